@@ -64,7 +64,8 @@ typedef enum {
   JEPA_B200_F32 = 0,
   JEPA_B200_F16 = 1,
   JEPA_B200_Q4_0 = 2, /* 32-element blocks: fp16 scale d + 16 bytes; byte j = q[j] | q[j+16] << 4; value (q-8)*d */
-  JEPA_B200_Q8_0 = 8  /* 32-element blocks: fp16 scale d + 32 x int8 q; value q*d */
+  JEPA_B200_Q8_0 = 8, /* 32-element blocks: fp16 scale d + 32 x int8 q; value q*d */
+  JEPA_B200_BF16 = 30 /* operands of the per-head calls below; no weight of the tensor table has it */
 } jepa_b200_dtype;
 
 typedef enum {
@@ -420,6 +421,123 @@ JEPA_B200_API int jepa_b200_op_mean_pool(const float *y, int B, int ntok, int D,
  * Returns OK, ERR_ARG, ERR_SHAPE or ERR_CUDA. */
 JEPA_B200_API int jepa_b200_op_mean_pool_noalloc(const float *y, int B, int ntok, int D, int first, float *out,
                                                  void *stream);
+
+/* ------------------------------------------------------------------------
+ * Per-head calls: rotary positions, norms of queries and keys, attention
+ * under masks.  They stand between a QKV projection and an output projection
+ * (jepa_b200_op_linear) and take their operands where these leave them: a
+ * tensor [B, N, heads, head_dim] is described by its strides, so that q, k
+ * and v may be views of one projection output [B, N, (hq + 2 hk) * head_dim]
+ * or of a cache.  They allocate nothing, keep nothing between calls and need
+ * no workspace: calls on several streams, and captured graphs of them, are
+ * independent of one another.  Forward only.
+ * ---------------------------------------------------------------------- */
+
+/* Element (b, n, h, i) of a [B, N, heads, head_dim] tensor lies at
+ * data[b * stride_b + n * stride_n + h * stride_h + i]; strides count
+ * elements, must not be negative, and may be 0 (a broadcast axis) for inputs.
+ * data and every stride are whole elements; what more a call needs of them
+ * it says itself. */
+typedef struct {
+  void *data;
+  int64_t stride_b, stride_n, stride_h;
+} jepa_b200_heads;
+
+typedef enum {
+  JEPA_B200_ROPE_HALF = 0,       /* pair i of a head: dims i and i + rot_dim / 2 */
+  JEPA_B200_ROPE_INTERLEAVED = 1 /* pair i of a head: dims 2i and 2i + 1 (the encoder's own rotation) */
+} jepa_b200_rope_layout;
+
+/* Rotary positions: pair i of the first rot_dim dims of every head of token
+ * (b, n) turns by pos[axis[i], b, n] * turns[i] * 2^-64 full turns,
+ *   (x0, x1) -> factor * (x0 cos - x1 sin, x0 sin + x1 cos),
+ * and the dims behind rot_dim stay as they are.  turns[i] is the fraction of
+ * a turn per unit of position as a binary fraction of 64 bits (radians per
+ * position / 2 pi * 2^64, rounded, modulo 2^64): the product with an integer
+ * position modulo 2^64 is exact, so far positions lose nothing. */
+typedef struct {
+  int rot_dim;              /* even, 0 (no rotation; every other member is then ignored) .. head_dim */
+  int layout;               /* jepa_b200_rope_layout */
+  int n_axes;               /* position axes, 1 .. 3 */
+  int pos_i64;              /* positions are int64 (1) or int32 (0) */
+  const void *pos;          /* device: element (a, b, n) at pos[a * pos_stride_axis + b * pos_stride_b + n] */
+  int64_t pos_stride_axis;
+  int64_t pos_stride_b;     /* 0: every clip has the same positions */
+  const uint64_t *turns;    /* device [rot_dim / 2] */
+  const uint8_t *axis;      /* device [rot_dim / 2], each < n_axes (others count as axis 0); may be NULL for one axis */
+  float factor;             /* on cosine and sine (1 for a plain rotation) */
+} jepa_b200_rope;
+
+/* Rotary positions of one tensor.  dtype F16, BF16 or F32 (x and out alike),
+ * head_dim 1 .. 256.  out may be x itself (the same data and strides); it
+ * must not overlap x in another way, nor the positions.  The angle, its
+ * cosine and sine and the rotation are f32; the result is rounded once.
+ * Errors: ERR_ARG, ERR_SHAPE, ERR_DTYPE, ERR_CUDA.  Nothing is done (OK) when
+ * B, N or heads is 0. */
+typedef struct {
+  jepa_b200_heads x, out;
+  int dtype, B, N, heads, head_dim;
+  jepa_b200_rope rope;
+} jepa_b200_rope_args;
+JEPA_B200_API int jepa_b200_op_rope(const jepa_b200_rope_args *a, void *stream);
+
+typedef enum {
+  JEPA_B200_NORM_RMS = 0,  /* y = x / sqrt(mean(x^2) + eps) * weight (+ bias) */
+  JEPA_B200_NORM_LAYER = 1 /* y = (x - mean) / sqrt(var + eps) * weight (+ bias) */
+} jepa_b200_norm;
+
+/* Norm of every head of q and of k over its head_dim values, then the
+ * rotation, in one pass and one launch: out = rope(norm(x)), f32 in between,
+ * rounded once.  Weights and biases are f32: [head_dim] shared by the heads
+ * (weight_stride_h 0) or [heads, head_dim] (weight_stride_h = elements from
+ * one head's to the next).  A bias may be NULL.  Types, sizes and aliasing as
+ * in jepa_b200_op_rope, for q and q_out and for k and k_out; no output may
+ * overlap another tensor's values.  eps >= 0.  Errors as there. */
+typedef struct {
+  jepa_b200_heads q, k, q_out, k_out;
+  int dtype, B, N, heads_q, heads_k, head_dim, norm;
+  float eps;
+  const float *q_weight, *q_bias, *k_weight, *k_bias; /* device */
+  int64_t q_weight_stride_h, q_bias_stride_h, k_weight_stride_h, k_bias_stride_h;
+  jepa_b200_rope rope;
+} jepa_b200_qk_norm_rope_args;
+JEPA_B200_API int jepa_b200_op_qk_norm_rope(const jepa_b200_qk_norm_rope_args *a, void *stream);
+
+/* Attention under masks.  Query head h reads key head h * heads_kv / heads_q
+ * (heads_q a multiple of heads_kv).  For query row i of clip b, at position
+ * p = q_start[b] + i among the keys, and key j:
+ *   s = scale * q.k;  cap > 0: s = cap * tanh(s / cap);
+ *   slopes: s -= slopes[h] * |p - j|;
+ *   out = sum_j exp(s) v / sum_j exp(s) over the allowed keys.
+ * The allowed keys of a row are one interval:
+ *   plain:  j < kv_len[b];
+ *   causal: also j <= p or j < prefix[b] (a prefix read in both directions);
+ *   documents (n_docs > 0; Nq = Nk): row b holds n_docs documents, document t
+ *     the tokens doc_offsets[b, t] .. doc_offsets[b, t + 1] - 1 (offsets not
+ *     decreasing; equal ones make an empty document).  Keys of the row's own
+ *     document, with causal those j <= i or within the first prefix[b, t]
+ *     tokens of it; kv_len and q_start are not read.
+ * A row without an allowed key gets zeros.  A row outside every document is
+ * not written.  Keys and values that a row may not read never reach it,
+ * whatever they hold (NaN, infinities).  kv_len is clamped to 0 .. Nk.
+ * dtype F16 or BF16; head_dim a multiple of 8, 8 .. 128; every data pointer
+ * 16-byte aligned and every stride a multiple of 8 elements.  Scores, softmax
+ * statistics and sums are f32; the probabilities are rounded to dtype for the
+ * product with v.  out must not overlap an input.  Nk may be 0 (zeros).
+ * Errors: ERR_ARG, ERR_SHAPE, ERR_DTYPE, ERR_CUDA; a device wait that ran
+ * out is reported by jepa_b200_op_sync_status. */
+typedef struct {
+  jepa_b200_heads q, k, v, out;
+  int dtype, B, Nq, Nk, heads_q, heads_kv, head_dim;
+  float scale, cap;           /* cap 0: none */
+  int causal, n_docs;
+  const float *slopes;        /* device [heads_q], or NULL */
+  const int32_t *prefix;      /* device [B], with documents [B, n_docs]; NULL: none.  Needs causal. */
+  const int32_t *doc_offsets; /* device [B, n_docs + 1]; NULL when n_docs is 0 */
+  const int32_t *kv_len;      /* device [B]; NULL: Nk */
+  const int32_t *q_start;     /* device [B]; NULL: Nk - Nq (the queries are the last tokens) */
+} jepa_b200_masked_attention_args;
+JEPA_B200_API int jepa_b200_op_masked_attention(const jepa_b200_masked_attention_args *a, void *stream);
 
 /* Synchronise `stream`, return and clear the device status of the op calls
  * (OK, ERR_TIMEOUT, ERR_CUDA). */

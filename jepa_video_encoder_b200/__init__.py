@@ -13,6 +13,7 @@ from typing import List, Optional, Tuple
 
 from . import _abi, synth
 from ._abi import JepaError, check, load_library
+from .heads import RopePlan, masked_attention, qk_norm_rope, rope, rope_plan
 
 POOLS = synth.POOL_IDS
 

@@ -4,13 +4,17 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from ctypes import (POINTER, c_char_p, c_double, c_float, c_int, c_int64, c_size_t, c_ulonglong, c_void_p)
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libjepa_b200.so")
 
+BF16 = 30  # dtype of the per-head calls besides the tensor table's ids
 OK, ERR_ARG, ERR_MISSING_TENSOR, ERR_SHAPE, ERR_DTYPE, ERR_CUDA, ERR_TIMEOUT, ERR_UNSUPPORTED = \
     0, -1, -2, -3, -4, -5, -6, -7
 EPI_F16, EPI_GELU_F16, EPI_RESID_F32, EPI_F32 = 0, 1, 2, 3
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+NORM_RMS, NORM_LAYER = 0, 1
 KERNEL_CLASSES = ("patch_embed", "layernorm", "gemm_qkv", "attention", "gemm_out", "gemm_up", "gemm_down",
                   "pool_head")
 
@@ -29,6 +33,60 @@ class Config(ctypes.Structure):
 class TensorEntry(ctypes.Structure):
     _fields_ = [("name", c_char_p), ("dtype", c_int), ("ndim", c_int), ("shape", c_int64 * 5),
                 ("data", c_void_p), ("nbytes", c_size_t)]
+
+
+class Heads(ctypes.Structure):
+    """jepa_b200_heads: a [B, N, heads, head_dim] operand."""
+    _fields_ = [("data", c_void_p), ("stride_b", c_int64), ("stride_n", c_int64), ("stride_h", c_int64)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("rot_dim", c_int), ("layout", c_int), ("n_axes", c_int), ("pos_i64", c_int), ("pos", c_void_p),
+                ("pos_stride_axis", c_int64), ("pos_stride_b", c_int64), ("turns", c_void_p), ("axis", c_void_p),
+                ("factor", c_float)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("x", Heads), ("out", Heads), ("dtype", c_int), ("B", c_int), ("N", c_int), ("heads", c_int),
+                ("head_dim", c_int), ("rope", Rope)]
+
+
+class QkNormRopeArgs(ctypes.Structure):
+    _fields_ = [("q", Heads), ("k", Heads), ("q_out", Heads), ("k_out", Heads), ("dtype", c_int), ("B", c_int),
+                ("N", c_int), ("heads_q", c_int), ("heads_k", c_int), ("head_dim", c_int), ("norm", c_int),
+                ("eps", c_float), ("q_weight", c_void_p), ("q_bias", c_void_p), ("k_weight", c_void_p),
+                ("k_bias", c_void_p), ("q_weight_stride_h", c_int64), ("q_bias_stride_h", c_int64),
+                ("k_weight_stride_h", c_int64), ("k_bias_stride_h", c_int64), ("rope", Rope)]
+
+
+class MaskedAttentionArgs(ctypes.Structure):
+    _fields_ = [("q", Heads), ("k", Heads), ("v", Heads), ("out", Heads), ("dtype", c_int), ("B", c_int),
+                ("Nq", c_int), ("Nk", c_int), ("heads_q", c_int), ("heads_kv", c_int), ("head_dim", c_int),
+                ("scale", c_float), ("cap", c_float), ("causal", c_int), ("n_docs", c_int), ("slopes", c_void_p),
+                ("prefix", c_void_p), ("doc_offsets", c_void_p), ("kv_len", c_void_p), ("q_start", c_void_p)]
+
+
+def packer(cls) -> struct.Struct:
+    """A struct.Struct that lays its values out as the ctypes structure ``cls``
+    does, nested structures flattened and pointers as integers (0: NULL): one
+    pack() costs a fraction of filling the structure, which counts for calls
+    of a few microseconds."""
+    code = {c_int: "i", c_int64: "q", c_float: "f", c_void_p: "Q"}
+
+    def leaves(c, base):
+        for name, typ in c._fields_:
+            at = base + getattr(c, name).offset
+            if issubclass(typ, ctypes.Structure):
+                yield from leaves(typ, at)
+            else:
+                yield at, typ
+
+    fmt, end = "=", 0
+    for at, typ in leaves(cls, 0):
+        fmt += f"{at - end}x" * (at > end) + code[typ]
+        end = at + ctypes.sizeof(typ)
+    pad = ctypes.sizeof(cls) - end
+    return struct.Struct(fmt + f"{pad}x" * (pad > 0))
 
 
 # name -> (restype, argtypes); every symbol the header declares
@@ -69,6 +127,10 @@ SIGNATURES = {
                                   c_void_p, c_int, c_void_p, c_void_p]),
     "jepa_b200_op_xattn_1q": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_void_p,
                                       c_void_p]),
+    # the structures may come as the bytes that packer() makes
+    "jepa_b200_op_rope": (c_int, [c_void_p, c_void_p]),
+    "jepa_b200_op_qk_norm_rope": (c_int, [c_void_p, c_void_p]),
+    "jepa_b200_op_masked_attention": (c_int, [c_void_p, c_void_p]),
     "jepa_b200_op_mean_pool": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_void_p]),
     "jepa_b200_op_mean_pool_noalloc": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_void_p]),
     "jepa_b200_op_sync_status": (c_int, [c_void_p]),

@@ -4,6 +4,7 @@
 
 #include <mutex>
 
+#include "head_ops.h"
 #include "internal.h"
 #include "patchify.h"
 
@@ -62,6 +63,69 @@ int make_matrix(DevMatrix* W, const void* w, const void* scales, int dtype, int 
   return JEPA_B200_OK;
 }
 
+// ---- per-head calls --------------------------------------------------------
+int dtype_bytes(int dtype) {
+  switch (dtype) {
+    case JEPA_B200_F32: return 4;
+    case JEPA_B200_F16:
+    case JEPA_B200_BF16: return 2;
+    default: return 0;
+  }
+}
+
+// The strides a [B, N, heads, d] operand can be read by; an axis of length 1
+// has no stride.
+bool heads_ok(const jepa_b200_heads& t, int elem_bytes) {
+  return t.data && (reinterpret_cast<uintptr_t>(t.data) & (elem_bytes - 1)) == 0 && t.stride_b >= 0 &&
+         t.stride_n >= 0 && t.stride_h >= 0 && t.stride_b < (1ll << 40) && t.stride_n < (1ll << 40) &&
+         t.stride_h < (1ll << 40);
+}
+// Outputs besides: no two elements in one place along a single axis.
+bool heads_out_ok(const jepa_b200_heads& t, int elem_bytes, int B, int N, int H, int d) {
+  return heads_ok(t, elem_bytes) && (B == 1 || t.stride_b >= d) && (N == 1 || t.stride_n >= d) &&
+         (H == 1 || t.stride_h >= d);
+}
+
+int fill_rope(RopeParams* r, const jepa_b200_rope& a, int d, int B) {
+  memset(r, 0, sizeof(*r));
+  if (a.rot_dim == 0) return JEPA_B200_OK;
+  if (a.layout != JEPA_B200_ROPE_HALF && a.layout != JEPA_B200_ROPE_INTERLEAVED) return JEPA_B200_ERR_ARG;
+  if (a.rot_dim < 0 || a.rot_dim % 2 != 0 || a.rot_dim > d || a.n_axes < 1 || a.n_axes > 3) return JEPA_B200_ERR_SHAPE;
+  if (!a.pos || !a.turns || (a.n_axes > 1 && !a.axis)) return JEPA_B200_ERR_ARG;
+  if ((a.pos_i64 != 0 && a.pos_i64 != 1) || (reinterpret_cast<uintptr_t>(a.pos) & (a.pos_i64 ? 7u : 3u)) != 0 ||
+      (reinterpret_cast<uintptr_t>(a.turns) & 7u) != 0)
+    return JEPA_B200_ERR_ARG;
+  if (a.pos_stride_axis < 0 || a.pos_stride_b < 0) return JEPA_B200_ERR_ARG;
+  r->rot_dim = a.rot_dim;
+  r->half_layout = a.layout == JEPA_B200_ROPE_HALF ? 1 : 0;
+  r->n_axes = a.n_axes;
+  r->pos_i64 = a.pos_i64;
+  r->pos = a.pos;
+  r->pos_stride_axis = a.n_axes > 1 ? a.pos_stride_axis : 0;
+  r->pos_stride_b = B > 1 ? a.pos_stride_b : 0;
+  r->turns = reinterpret_cast<const unsigned long long*>(a.turns);
+  r->axis = a.n_axes > 1 ? a.axis : nullptr;
+  r->factor = a.factor;
+  return JEPA_B200_OK;
+}
+
+int fill_tensor(HeadTensor* t, const jepa_b200_heads& in, const jepa_b200_heads& out, int elem_bytes, int B, int N,
+                int H, int d) {
+  if (!heads_ok(in, elem_bytes) || !heads_out_ok(out, elem_bytes, B, N, H, d)) return JEPA_B200_ERR_ARG;
+  t->in = in.data;
+  t->out = out.data;
+  t->in_b = in.stride_b;
+  t->in_n = in.stride_n;
+  t->in_h = in.stride_h;
+  t->out_b = out.stride_b;
+  t->out_n = out.stride_n;
+  t->out_h = out.stride_h;
+  t->heads = H;
+  return JEPA_B200_OK;
+}
+
+bool float_ptr_ok(const float* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 }  // namespace
 
 extern "C" {
@@ -78,6 +142,9 @@ int jepa_b200_op_sync_status(void* stream) {
     cudaMemset(e, 0, sizeof(DevErr));
     return h.code == DERR_TIMEOUT ? JEPA_B200_ERR_TIMEOUT : JEPA_B200_ERR_CUDA;
   }
+  unsigned code = 0;
+  if (masked_attention_take_error(&code) != JEPA_B200_OK) return JEPA_B200_ERR_CUDA;
+  if (code != DERR_NONE) return code == DERR_TIMEOUT ? JEPA_B200_ERR_TIMEOUT : JEPA_B200_ERR_CUDA;
   return JEPA_B200_OK;
 }
 
@@ -246,6 +313,127 @@ int jepa_b200_op_xattn_1q(const float* q, const void* k, const void* vt, int B, 
   if (!aligned16(k)) return JEPA_B200_ERR_ARG;
   return launch_xattn_1q(q, static_cast<const __half*>(k), static_cast<const __half*>(vt), B, heads, ntok, npad, out,
                          static_cast<cudaStream_t>(stream));
+}
+
+int jepa_b200_op_rope(const jepa_b200_rope_args* a, void* stream) {
+  if (!a) return JEPA_B200_ERR_ARG;
+  const int es = dtype_bytes(a->dtype);
+  if (!es) return JEPA_B200_ERR_DTYPE;
+  if (a->B < 0 || a->N < 0 || a->heads < 0 || a->head_dim < 1 || a->head_dim > kMaxHeadDim ||
+      static_cast<long long>(a->B) * a->N > 0x7fffffffll)
+    return JEPA_B200_ERR_SHAPE;
+  if (a->B == 0 || a->N == 0 || a->heads == 0) return JEPA_B200_OK;
+  HeadOpParams p;
+  memset(&p, 0, sizeof(p));
+  int s = fill_rope(&p.rope, a->rope, a->head_dim, a->B);
+  if (s) return s;
+  if ((s = fill_tensor(&p.t[0], a->x, a->out, es, a->B, a->N, a->heads, a->head_dim))) return s;
+  p.B = a->B;
+  p.N = a->N;
+  p.d = a->head_dim;
+  p.norm = NORM_NONE;
+  return launch_head_op(p, a->dtype, static_cast<cudaStream_t>(stream));
+}
+
+int jepa_b200_op_qk_norm_rope(const jepa_b200_qk_norm_rope_args* a, void* stream) {
+  if (!a) return JEPA_B200_ERR_ARG;
+  const int es = dtype_bytes(a->dtype);
+  if (!es) return JEPA_B200_ERR_DTYPE;
+  if (a->B < 0 || a->N < 0 || a->heads_q < 0 || a->heads_k < 0 || a->head_dim < 1 || a->head_dim > kMaxHeadDim ||
+      static_cast<long long>(a->B) * a->N > 0x7fffffffll ||
+      static_cast<long long>(a->heads_q) + a->heads_k > 0x7fffffffll)
+    return JEPA_B200_ERR_SHAPE;
+  if (a->norm != JEPA_B200_NORM_RMS && a->norm != JEPA_B200_NORM_LAYER) return JEPA_B200_ERR_ARG;
+  if (!(a->eps >= 0.0f)) return JEPA_B200_ERR_ARG;
+  if (a->B == 0 || a->N == 0 || (a->heads_q == 0 && a->heads_k == 0)) return JEPA_B200_OK;
+  HeadOpParams p;
+  memset(&p, 0, sizeof(p));
+  int s = fill_rope(&p.rope, a->rope, a->head_dim, a->B);
+  if (s) return s;
+  int n = 0;
+  const struct {
+    const jepa_b200_heads *in, *out;
+    int heads;
+    const float *weight, *bias;
+    int64_t weight_h, bias_h;
+  } side[2] = {{&a->q, &a->q_out, a->heads_q, a->q_weight, a->q_bias, a->q_weight_stride_h, a->q_bias_stride_h},
+               {&a->k, &a->k_out, a->heads_k, a->k_weight, a->k_bias, a->k_weight_stride_h, a->k_bias_stride_h}};
+  for (const auto& x : side) {
+    if (x.heads == 0) continue;
+    if (!x.weight || !float_ptr_ok(x.weight) || !float_ptr_ok(x.bias) || x.weight_h < 0 || x.bias_h < 0)
+      return JEPA_B200_ERR_ARG;
+    HeadTensor& t = p.t[n++];
+    if ((s = fill_tensor(&t, *x.in, *x.out, es, a->B, a->N, x.heads, a->head_dim))) return s;
+    t.weight = x.weight;
+    t.bias = x.bias;
+    t.weight_h = x.weight_h;
+    t.bias_h = x.bias_h;
+  }
+  p.B = a->B;
+  p.N = a->N;
+  p.d = a->head_dim;
+  p.norm = a->norm == JEPA_B200_NORM_RMS ? NORM_RMS : NORM_LAYER;
+  p.eps = a->eps;
+  return launch_head_op(p, a->dtype, static_cast<cudaStream_t>(stream));
+}
+
+int jepa_b200_op_masked_attention(const jepa_b200_masked_attention_args* a, void* stream) {
+  if (!a) return JEPA_B200_ERR_ARG;
+  if (a->dtype != JEPA_B200_F16 && a->dtype != JEPA_B200_BF16) return JEPA_B200_ERR_DTYPE;
+  if (a->B < 0 || a->Nq < 0 || a->Nk < 0 || a->heads_q < 1 || a->heads_kv < 1 || a->heads_q % a->heads_kv != 0 ||
+      a->head_dim < 8 || a->head_dim > 128 || a->head_dim % 8 != 0 || a->B > 65535 || a->heads_q > 65535 ||
+      static_cast<long long>(a->B) * a->heads_q > 0x7fffffffll || a->Nq > 0x3fffffff || a->Nk > 0x3fffffff)
+    return JEPA_B200_ERR_SHAPE;
+  if (!(a->scale == a->scale) || !(a->cap >= 0.0f) || (a->causal != 0 && a->causal != 1)) return JEPA_B200_ERR_ARG;
+  if (a->n_docs < 0 || (a->n_docs > 0) != (a->doc_offsets != nullptr) || (a->prefix && !a->causal))
+    return JEPA_B200_ERR_ARG;
+  if (a->n_docs > 0 && (a->Nq != a->Nk || a->kv_len || a->q_start)) return JEPA_B200_ERR_ARG;
+  for (const void* x : {static_cast<const void*>(a->slopes), static_cast<const void*>(a->prefix),
+                        static_cast<const void*>(a->doc_offsets), static_cast<const void*>(a->kv_len),
+                        static_cast<const void*>(a->q_start)})
+    if ((reinterpret_cast<uintptr_t>(x) & 3u) != 0) return JEPA_B200_ERR_ARG;
+  if (a->B == 0 || a->Nq == 0) return JEPA_B200_OK;
+  for (const jepa_b200_heads* t : {&a->q, &a->k, &a->v, &a->out}) {
+    if (a->Nk == 0 && (t == &a->k || t == &a->v)) continue;  // nothing to read
+    if (!heads_ok(*t, 2) || !aligned16(t->data) || t->stride_b % 8 != 0 || t->stride_n % 8 != 0 || t->stride_h % 8 != 0)
+      return JEPA_B200_ERR_ARG;
+  }
+  if (!heads_out_ok(a->out, 2, a->B, a->Nq, a->heads_q, a->head_dim)) return JEPA_B200_ERR_ARG;
+  MaskedAttnParams p;
+  memset(&p, 0, sizeof(p));
+  p.q = static_cast<const uint16_t*>(a->q.data);
+  p.k = static_cast<const uint16_t*>(a->k.data);
+  p.v = static_cast<const uint16_t*>(a->v.data);
+  p.out = static_cast<uint16_t*>(a->out.data);
+  p.q_b = a->q.stride_b;
+  p.q_n = a->q.stride_n;
+  p.q_h = a->q.stride_h;
+  p.k_b = a->k.stride_b;
+  p.k_n = a->k.stride_n;
+  p.k_h = a->k.stride_h;
+  p.v_b = a->v.stride_b;
+  p.v_n = a->v.stride_n;
+  p.v_h = a->v.stride_h;
+  p.o_b = a->out.stride_b;
+  p.o_n = a->out.stride_n;
+  p.o_h = a->out.stride_h;
+  p.B = a->B;
+  p.Nq = a->Nq;
+  p.Nk = a->Nk;
+  p.hq = a->heads_q;
+  p.hk = a->heads_kv;
+  p.d = a->head_dim;
+  p.scale = a->scale;
+  p.cap = a->cap;
+  p.causal = a->causal;
+  p.n_docs = a->n_docs;
+  p.slopes = a->slopes;
+  p.prefix = a->prefix;
+  p.doc_offsets = a->doc_offsets;
+  p.kv_len = a->kv_len;
+  p.q_start = a->q_start;
+  p.timeout_ns = g_timeout_ns;
+  return launch_masked_attention(p, a->dtype == JEPA_B200_BF16, static_cast<cudaStream_t>(stream));
 }
 
 int jepa_b200_op_mean_pool(const float* y, int B, int ntok, int D, int first, float* out, void* stream) {

@@ -1,0 +1,487 @@
+"""Per-head operators of a transformer block, between its QKV projection and
+its output projection: rotary positions (rope), norms of queries and keys with
+the rotation in the same pass (qk_norm_rope), and attention under masks
+(masked_attention).
+
+Operands are CUDA tensors [B, N, heads, head_dim] with a contiguous last axis,
+views of one projection output or of a cache included.  The calls are
+asynchronous on ``stream`` (default: the current stream), allocate nothing but
+an output that was not given, keep nothing between calls, and can be captured
+into CUDA graphs.  They are forward only: a tensor that requires grad is
+refused while autograd records.
+"""
+from __future__ import annotations
+
+import math
+from dataclasses import dataclass
+from typing import Any, Optional, Sequence, Tuple
+
+from . import _abi
+from ._abi import check, load_library
+
+_ROPE = _abi.packer(_abi.RopeArgs)
+_QK = _abi.packer(_abi.QkNormRopeArgs)
+_ATTN = _abi.packer(_abi.MaskedAttentionArgs)
+_LAYOUTS = {"half": _abi.ROPE_HALF, "interleaved": _abi.ROPE_INTERLEAVED}
+_NORMS = {"rms": _abi.NORM_RMS, "layer": _abi.NORM_LAYER}
+_NO_ROPE = (0, 0, 0, 0, 0, 0, 0, 0, 0, 0.0)
+_dtype_ids = {}
+
+
+def _ids():
+    if not _dtype_ids:
+        import torch
+        _dtype_ids.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: _abi.BF16})
+    return _dtype_ids
+
+
+# ---------------------------------------------------------------- operands
+def _check_cuda(t, name: str, device: int) -> None:
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
+    if t.device.index != device:
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{device}")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires grad: the per-head operators are forward only (call them under "
+                         "torch.no_grad() or on detached tensors)")
+
+
+def check_heads(t, name: str, dtype=None, shape: Optional[Sequence[int]] = None, granule: int = 1) -> None:
+    """Validate the layout of a [B, N, heads, head_dim] operand: four axes,
+    the last one contiguous; ``dtype`` and ``shape`` where they are set by
+    another operand; with ``granule`` g > 1 a data pointer and strides that
+    are multiples of g elements."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [B, N, heads, head_dim], got {list(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.stride(3) != 1 and t.shape[3] > 1:
+        raise ValueError(f"{name} must have a contiguous last axis")
+    if granule > 1 and t.numel():
+        if t.data_ptr() % (granule * t.element_size()):
+            raise ValueError(f"{name} must start at a multiple of {granule * t.element_size()} bytes")
+        for n, s in zip(t.shape[:3], t.stride()[:3]):
+            if n > 1 and s % granule:
+                raise ValueError(f"{name}'s strides must be multiples of {granule} elements, got {t.stride()}")
+
+
+def _span(t) -> int:
+    """Elements from a view's first to behind its last."""
+    return 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+
+
+def check_output(out, name: str, inputs) -> None:
+    """Validate an output that the caller gave: no two of its elements in one
+    place, and no overlap with ``inputs``, a list of (tensor, name, may be the
+    output itself).  Views whose ranges of memory interleave count as
+    overlapping unless their elements can be told apart by their rows."""
+    axes = sorted((s, n) for n, s in zip(out.shape, out.stride()) if n > 1)
+    reach = 1
+    for s, n in axes:
+        if s < reach:
+            raise ValueError(f"{name} has elements that share memory (strides {out.stride()})")
+        reach = s * (n - 1) + reach
+    for t, what, same_ok in inputs:
+        if t is None or not t.numel() or not out.numel():
+            continue
+        if out.untyped_storage().data_ptr() != t.untyped_storage().data_ptr():
+            continue
+        if same_ok and out.data_ptr() == t.data_ptr() and out.dtype == t.dtype and \
+                all(a == b for n, a, b in zip(out.shape, out.stride(), t.stride()) if n > 1):
+            continue
+        o0, t0 = out.data_ptr(), t.data_ptr()
+        o1, t1 = o0 + _span(out) * out.element_size(), t0 + _span(t) * t.element_size()
+        if o1 <= t0 or t1 <= o0:
+            continue
+        if not _rows_apart(out, t):
+            raise ValueError(f"{name} overlaps {what}")
+
+
+def _rows_apart(a, b) -> bool:
+    """Whether two [B, N, h, d] views step through memory in the same rows and
+    lie in separate columns of them, as slices of one projection output do."""
+    if a.dim() != 4 or b.dim() != 4 or a.dtype != b.dtype:
+        return False
+    axis = 1 if max(a.shape[1], b.shape[1]) > 1 else 0  # one token a clip: the rows are the clips
+    row = a.stride(axis)
+    if min(a.shape[axis], b.shape[axis]) < 2 or row != b.stride(axis) or row < 1:
+        return False
+    off, wide = (b.data_ptr() - a.data_ptr()) // a.element_size() % row, []
+    for x in (a, b):
+        if axis == 1 and x.shape[0] > 1 and x.stride(0) % row:
+            return False
+        wide.append(1 + sum((n - 1) * s for n, s in zip(x.shape[2:], x.stride()[2:])))
+    return wide[0] <= off and off + wide[1] <= row
+
+
+def _strides(t) -> Tuple[int, int, int, int]:
+    s = t.stride()
+    return t.data_ptr(), s[0], s[1], s[2]
+
+
+def _launch(stream):
+    """(current device, raw stream) of a call."""
+    import torch
+    device = torch.cuda.current_device()
+    if stream is None:
+        return device, torch.cuda.current_stream().cuda_stream
+    if stream.device_index != device:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, but the current device is cuda:{device}")
+    return device, stream.cuda_stream
+
+
+def _new(like_shape, dtype, device: int, stream, zero: bool = False):
+    """An output of the call, owned by the stream that writes it."""
+    import torch
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(like_shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(like_shape, dtype=dtype, device=device)
+
+
+# -------------------------------------------------------------- rotary plan
+@dataclass(frozen=True)
+class RopePlan:
+    """Frequencies of a rotation on one device (rope_plan makes it; a program
+    keeps it).  pairs of dims turn by position * inv_freq radians."""
+    rot_dim: int
+    layout: str
+    sections: Tuple[int, ...]
+    inv_freq: Tuple[float, ...]   # radians per unit of position, one a pair
+    factor: float                 # on cosine and sine
+    turns: Any                    # device int64 [pairs]: inv_freq / 2 pi as 64-bit binary fractions
+    axis: Any                     # device uint8 [pairs], None for one axis
+    device: int
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, sections: Optional[Sequence[int]] = None,
+                     scaling: Optional[dict] = None):
+    """(inverse frequencies, axis of each pair, factor on cosine and sine).
+
+    The pairs form one section per position axis (default: one section of
+    rot_dim / 2).  Pair i of a section of n turns by base^(-i/n) radians per
+    position.  ``scaling`` stretches that for long contexts, with "factor" f:
+      {"type": "linear"}: every frequency / f;
+      {"type": "ntk"}: base * f^(n/(n-1)), so that the slowest pair turns f
+        times slower and the fastest as before;
+      {"type": "yarn", "original": L, "fast": 32, "slow": 1, "magnitude": m}: a
+        pair that makes r turns within the L positions of training keeps its
+        frequency for r >= fast, has it divided by f for r <= slow, and is
+        blended linearly in r between; cosine and sine are multiplied by m
+        (default 1 + 0.1 ln f)."""
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError(f"rot_dim must be even and at least 2, got {rot_dim}")
+    sections = (rot_dim // 2,) if sections is None else tuple(int(n) for n in sections)
+    if not 1 <= len(sections) <= 3 or min(sections) < 1 or sum(sections) != rot_dim // 2:
+        raise ValueError(f"sections must be 1 to 3 positive counts of pairs that add up to {rot_dim // 2}, got {sections}")
+    if not (base > 0 and math.isfinite(base)):
+        raise ValueError(f"base must be positive, got {base}")
+    kind, f, factor = None, 1.0, 1.0
+    if scaling is not None:
+        kind, f = scaling.get("type"), float(scaling.get("factor", 1.0))
+        known = {"linear": set(), "ntk": set(), "yarn": {"original", "fast", "slow", "magnitude"}}
+        if kind not in known:
+            raise ValueError(f"scaling type must be one of {sorted(known)}, got {kind!r}")
+        if set(scaling) - known[kind] - {"type", "factor"}:
+            raise ValueError(f"unknown keys in scaling: {sorted(set(scaling) - known[kind] - {'type', 'factor'})}")
+        if not (f > 0 and math.isfinite(f)):
+            raise ValueError(f"scaling factor must be positive, got {f}")
+    freq, axis = [], []
+    for a, n in enumerate(sections):
+        b = base
+        if kind == "ntk":
+            if n < 2:
+                raise ValueError("ntk scaling needs sections of two pairs or more")
+            b = base * f ** (n / (n - 1))
+        freq += [b ** (-i / n) for i in range(n)]
+        axis += [a] * n
+    if kind == "linear":
+        freq = [w / f for w in freq]
+    elif kind == "yarn":
+        if "original" not in scaling:
+            raise ValueError('yarn scaling needs "original", the positions of training')
+        length, fast, slow = float(scaling["original"]), float(scaling.get("fast", 32.0)), float(scaling.get("slow", 1.0))
+        if not (length > 0 and fast > slow >= 0):
+            raise ValueError("yarn scaling needs original > 0 and fast > slow >= 0")
+        keep = [min(1.0, max(0.0, (length * w / (2 * math.pi) - slow) / (fast - slow))) for w in freq]
+        freq = [w * (g + (1 - g) / f) for w, g in zip(freq, keep)]
+        factor = float(scaling.get("magnitude", 1.0 + 0.1 * math.log(f)))
+    return tuple(freq), tuple(axis), factor
+
+
+def rope_turns(inv_freq: Sequence[float]):
+    """Radians per position as signed 64-bit words: the fraction of a turn per
+    position times 2^64, rounded, modulo 2^64."""
+    words = [int(round(math.ldexp(math.fmod(w / (2 * math.pi), 1.0), 64))) % (1 << 64) for w in inv_freq]
+    return [w - (1 << 64) if w >= 1 << 63 else w for w in words]
+
+
+def rope_plan(rot_dim: int, *, layout: str = "half", base: float = 10000.0, sections: Optional[Sequence[int]] = None,
+              scaling: Optional[dict] = None, device: Optional[int] = None) -> RopePlan:
+    """Plan of a rotation of the first rot_dim dims of every head.
+
+    layout "half": pair i is dims (i, i + rot_dim / 2); "interleaved": dims
+    (2i, 2i + 1).  sections: pairs of each position axis (the encoder's own
+    3-D rotation is rope_plan(60, layout="interleaved", sections=(10, 10,
+    10))).  base, scaling: see rope_frequencies.  device: index of the CUDA
+    device (default: the current one)."""
+    import torch
+    if layout not in _LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
+    freq, axis, factor = rope_frequencies(rot_dim, base, sections, scaling)
+    sections = (rot_dim // 2,) if sections is None else tuple(int(n) for n in sections)
+    device = torch.cuda.current_device() if device is None else int(device)
+    turns = torch.tensor(rope_turns(freq), dtype=torch.int64, device=f"cuda:{device}")
+    axes = torch.tensor(axis, dtype=torch.uint8, device=f"cuda:{device}") if len(sections) > 1 else None
+    return RopePlan(rot_dim, layout, sections, freq, factor, turns, axes, device)
+
+
+def check_positions(positions, n_axes: int, B: int, N: int) -> Tuple[int, int, int]:
+    """Validate positions: int32 or int64, [N] or [B, N] for one axis, [axes,
+    N] or [axes, B, N] for more, the token axis contiguous.  Returns (is
+    int64, axis stride, batch stride)."""
+    import torch
+    if not isinstance(positions, torch.Tensor):
+        raise TypeError(f"positions must be a torch.Tensor, got {type(positions).__name__}")
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"positions must be int32 or int64, got {positions.dtype}")
+    shape = positions.shape
+    lead = () if n_axes == 1 else (n_axes,)
+    if shape == lead + (N,):
+        batched = False
+    elif shape == lead + (B, N):
+        batched = True
+    else:
+        raise ValueError(f"positions must be {list(lead + (N,))} or {list(lead + (B, N))}, got {list(shape)}")
+    if N > 1 and positions.stride(-1) != 1:
+        raise ValueError("positions must be contiguous along the tokens")
+    return (1 if positions.dtype == torch.int64 else 0, positions.stride(0) if n_axes > 1 else 0,
+            positions.stride(-2) if batched else 0)
+
+
+def _rope_words(plan: RopePlan, positions, B: int, N: int, d: int, device: int):
+    if not isinstance(plan, RopePlan):
+        raise TypeError(f"plan must be a RopePlan, got {type(plan).__name__}")
+    if plan.rot_dim > d:
+        raise ValueError(f"the plan turns {plan.rot_dim} dims of heads that have {d}")
+    axes = len(plan.sections)
+    i64, stride_axis, stride_b = check_positions(positions, axes, B, N)
+    _check_cuda(positions, "positions", device)
+    if plan.device != device:
+        raise ValueError(f"the plan is on cuda:{plan.device}, but the current device is cuda:{device}")
+    return (plan.rot_dim, _LAYOUTS[plan.layout], axes, i64, positions.data_ptr(), stride_axis, stride_b,
+            plan.turns.data_ptr(), 0 if plan.axis is None else plan.axis.data_ptr(), plan.factor)
+
+
+def _float_type(t, name: str) -> int:
+    ids = _ids()
+    if t.dtype not in ids:
+        raise ValueError(f"{name} must be float16, bfloat16 or float32, got {t.dtype}")
+    return ids[t.dtype]
+
+
+def rope(x, positions, plan: RopePlan, out=None, stream=None):
+    """Rotary positions: x [B, N, heads, head_dim] float16, bfloat16 or
+    float32, head_dim up to 256 -> a tensor like x.
+
+    positions: integer tensor [N] (every clip the same) or [B, N], with
+    several axes [axes, N] or [axes, B, N].  out: the tensor to write; x
+    itself turns x in place."""
+    check_heads(x, "x")
+    B, N, H, d = x.shape
+    dtype = _float_type(x, "x")
+    device, raw = _launch(stream)
+    _check_cuda(x, "x", device)
+    if not 1 <= d <= 256:
+        raise ValueError(f"head_dim must be 1 to 256, got {d}")
+    words = _rope_words(plan, positions, B, N, d, device)
+    if out is None:
+        out = _new(x.shape, x.dtype, device, stream)
+    else:
+        check_heads(out, "out", x.dtype, x.shape)
+        _check_cuda(out, "out", device)
+        check_output(out, "out", [(x, "x", True), (positions, "positions", False)])
+    if not x.numel():
+        return out
+    check(load_library().jepa_b200_op_rope(_ROPE.pack(*_strides(x), *_strides(out), dtype, B, N, H, d, *words), raw),
+          "rope")
+    return out
+
+
+def _weight(t, name: str, heads: int, d: int, device: int) -> Tuple[int, int]:
+    import torch
+    if t is None:
+        return 0, 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != torch.float32:
+        raise ValueError(f"{name} must be float32, got {t.dtype}")
+    if tuple(t.shape) not in ((d,), (heads, d)) or (d > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be [{d}] or [{heads}, {d}] with a contiguous last axis, got {list(t.shape)}")
+    _check_cuda(t, name, device)
+    return t.data_ptr(), t.stride(0) if t.dim() == 2 else 0
+
+
+def qk_norm_rope(q, k, positions, plan: Optional[RopePlan], q_weight, k_weight, *, q_bias=None, k_bias=None,
+                 norm: str = "rms", eps: float = 1e-6, q_out=None, k_out=None, stream=None):
+    """Norm of every head of q [B, N, hq, d] and k [B, N, hk, d], then the
+    rotation, in one launch.  Returns (q_out, k_out), tensors like q and k.
+
+    norm "rms": x / sqrt(mean(x^2) + eps) * weight (+ bias); "layer": (x -
+    mean) / sqrt(var + eps) * weight (+ bias).  Weights and biases: float32
+    [d], or [heads, d] of their own.  plan None (positions then None too):
+    no rotation.  q_out, k_out: the tensors to write; q and k themselves for
+    an update in place, or rows of a cache."""
+    check_heads(q, "q")
+    dtype = _float_type(q, "q")
+    check_heads(k, "k", q.dtype)
+    B, N, hq, d = q.shape
+    hk = k.shape[2]
+    if tuple(k.shape) != (B, N, hk, d):
+        raise ValueError(f"k must be [{B}, {N}, heads, {d}] like q, got {list(k.shape)}")
+    if norm not in _NORMS:
+        raise ValueError(f"norm must be one of {sorted(_NORMS)}, got {norm!r}")
+    if not (eps >= 0):
+        raise ValueError(f"eps must not be negative, got {eps}")
+    if not 1 <= d <= 256:
+        raise ValueError(f"head_dim must be 1 to 256, got {d}")
+    device, raw = _launch(stream)
+    _check_cuda(q, "q", device)
+    _check_cuda(k, "k", device)
+    if q_weight is None or k_weight is None:
+        raise TypeError("q_weight and k_weight must be tensors")
+    qw, qw_h = _weight(q_weight, "q_weight", hq, d, device)
+    kw, kw_h = _weight(k_weight, "k_weight", hk, d, device)
+    qb, qb_h = _weight(q_bias, "q_bias", hq, d, device)
+    kb, kb_h = _weight(k_bias, "k_bias", hk, d, device)
+    if plan is None:
+        if positions is not None:
+            raise ValueError("positions need a plan")
+        words = _NO_ROPE
+    else:
+        words = _rope_words(plan, positions, B, N, d, device)
+    others = [(positions, "positions", False), (q_weight, "q_weight", False), (k_weight, "k_weight", False),
+              (q_bias, "q_bias", False), (k_bias, "k_bias", False)]
+    if q_out is None:
+        q_out = _new(q.shape, q.dtype, device, stream)
+    else:
+        check_heads(q_out, "q_out", q.dtype, q.shape)
+        _check_cuda(q_out, "q_out", device)
+        check_output(q_out, "q_out", [(q, "q", True), (k, "k", False)] + others)
+    if k_out is None:
+        k_out = _new(k.shape, k.dtype, device, stream)
+    else:
+        check_heads(k_out, "k_out", q.dtype, k.shape)
+        _check_cuda(k_out, "k_out", device)
+        check_output(k_out, "k_out", [(k, "k", True), (q, "q", False), (q_out, "q_out", False)] + others)
+    if not q.numel() and not k.numel():
+        return q_out, k_out
+    check(load_library().jepa_b200_op_qk_norm_rope(
+        _QK.pack(*_strides(q), *_strides(k), *_strides(q_out), *_strides(k_out), dtype, B, N, hq, hk, d, _NORMS[norm],
+                 eps, qw, qb, kw, kb, qw_h, qb_h, kw_h, kb_h, *words), raw), "qk_norm_rope")
+    return q_out, k_out
+
+
+def _per_clip(t, name: str, shape, device: int) -> int:
+    """Device address of an int32 tensor that a kernel indexes per clip."""
+    import torch
+    if t is None:
+        return 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)}, got {t.dtype} {list(t.shape)}")
+    _check_cuda(t, name, device)
+    return t.data_ptr()
+
+
+def masked_attention(q, k, v, *, scale: Optional[float] = None, cap: Optional[float] = None, slopes=None,
+                     causal: bool = False, prefix=None, doc_offsets=None, kv_len=None, q_start=None, out=None,
+                     stream=None):
+    """Attention of q [B, Nq, hq, d] over k, v [B, Nk, hk, d] (float16 or
+    bfloat16, d a multiple of 8 up to 128, hq a multiple of hk: query head h
+    reads key head h * hk // hq) -> [B, Nq, hq, d].
+
+    Query row i of clip b stands at position p = q_start[b] + i among the
+    keys (int32 [B]; default Nk - Nq: the queries are the last tokens).
+      s = scale * q.k (default 1 / sqrt(d)); cap c: s = c * tanh(s / c);
+      slopes float32 [hq]: s -= slopes[h] * |p - j| for key j;
+      kv_len int32 [B]: only keys j < kv_len[b] (a padded batch, a cache);
+      causal: only keys j <= p; prefix int32 [B]: or j < prefix[b];
+      doc_offsets int32 [B, n + 1] (needs Nq = Nk, no kv_len or q_start): a
+        row of n documents one after another, document t the tokens
+        doc_offsets[b, t] .. doc_offsets[b, t + 1] - 1 (never decreasing;
+        equal offsets make an empty one), each reading itself alone; prefix
+        is then [B, n] and counts from each document's start.
+    Rows that may read no key are zeros.  Rows outside every document are
+    left as they are in ``out``, and are zeros where out is not given.  Keys
+    and values that a row may not read do not reach it, whatever they hold."""
+    import torch
+    check_heads(q, "q", granule=8)
+    if q.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"q must be float16 or bfloat16, got {q.dtype}")
+    dtype = _ids()[q.dtype]
+    check_heads(k, "k", q.dtype, granule=8)
+    check_heads(v, "v", q.dtype, k.shape, granule=8)
+    B, Nq, hq, d = q.shape
+    _, Nk, hk, _ = k.shape
+    if k.shape[0] != B or k.shape[3] != d:
+        raise ValueError(f"k must be [{B}, Nk, heads, {d}] like q, got {list(k.shape)}")
+    if hq < 1 or hk < 1 or hq % hk:
+        raise ValueError(f"q's heads must be a multiple of k's, got {hq} and {hk}")
+    if not 8 <= d <= 128 or d % 8:
+        raise ValueError(f"head_dim must be a multiple of 8 from 8 to 128, got {d}")
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    cap = 0.0 if cap is None else float(cap)
+    if not math.isfinite(scale):
+        raise ValueError(f"scale must be finite, got {scale}")
+    if not (cap >= 0 and math.isfinite(cap)):
+        raise ValueError(f"cap must be finite and not negative, got {cap}")
+    if prefix is not None and not causal:
+        raise ValueError("prefix needs causal")
+    device, raw = _launch(stream)
+    _check_cuda(q, "q", device)
+    _check_cuda(k, "k", device)
+    _check_cuda(v, "v", device)
+    n_docs = 0
+    if doc_offsets is not None:
+        if kv_len is not None or q_start is not None:
+            raise ValueError("doc_offsets exclude kv_len and q_start")
+        if Nq != Nk:
+            raise ValueError(f"doc_offsets need as many queries as keys, got {Nq} and {Nk}")
+        if not isinstance(doc_offsets, torch.Tensor) or doc_offsets.dim() != 2 or doc_offsets.shape[1] < 2:
+            raise ValueError("doc_offsets must be an int32 tensor [B, n + 1] with n >= 1")
+        n_docs = doc_offsets.shape[1] - 1
+    at_docs = _per_clip(doc_offsets, "doc_offsets", (B, n_docs + 1), device)
+    at_prefix = _per_clip(prefix, "prefix", (B, n_docs) if n_docs else (B,), device)
+    at_len = _per_clip(kv_len, "kv_len", (B,), device)
+    at_start = _per_clip(q_start, "q_start", (B,), device)
+    at_slopes = 0
+    if slopes is not None:
+        at_slopes, _ = _weight(slopes, "slopes", 1, hq, device)
+        if slopes.dim() != 1:
+            raise ValueError(f"slopes must be [{hq}], got {list(slopes.shape)}")
+    if out is None:
+        out = _new(q.shape, q.dtype, device, stream, zero=n_docs > 0)
+    else:
+        check_heads(out, "out", q.dtype, q.shape, granule=8)
+        _check_cuda(out, "out", device)
+        check_output(out, "out", [(q, "q", False), (k, "k", False), (v, "v", False), (prefix, "prefix", False),
+                                  (doc_offsets, "doc_offsets", False), (kv_len, "kv_len", False),
+                                  (q_start, "q_start", False), (slopes, "slopes", False)])
+    if not q.numel():
+        return out
+    check(load_library().jepa_b200_op_masked_attention(
+        _ATTN.pack(*_strides(q), *_strides(k), *_strides(v), *_strides(out), dtype, B, Nq, Nk, hq, hk, d, scale, cap,
+                   1 if causal else 0, n_docs, at_slopes, at_prefix, at_docs, at_len, at_start), raw),
+        "masked_attention")
+    return out
