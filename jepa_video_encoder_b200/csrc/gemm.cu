@@ -1151,8 +1151,9 @@ bool make_tmap_f16(CUtensorMap* m, const void* base, int rank, const uint64_t* d
                    const uint32_t* box) {
   auto fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t d[3], s[2];
-  cuuint32_t b[3], es[3] = {1, 1, 1};
+  cuuint64_t d[5], s[4];
+  cuuint32_t b[5], es[5] = {1, 1, 1, 1, 1};
+  if (rank < 1 || rank > 5) return false;
   for (int i = 0; i < rank; ++i) {
     d[i] = dims[i];
     b[i] = box[i];

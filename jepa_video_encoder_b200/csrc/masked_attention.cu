@@ -140,6 +140,616 @@ __global__ void __launch_bounds__(128) masked_rows_kernel(const MaskedAttnParams
   if (r.written) attend_row<BF>(p, b, i, h, r, lane);
 }
 
+// ------------------------------------------------------------ tensor cores --
+// 128-query tiles on tcgen05.  A work item is 256 query rows (two tiles) of
+// one head; one persistent CTA an SM walks items with a fixed stride.
+//   warps 0-3, 4-7  softmax of tile 0 and of tile 1, one thread a row: the
+//                   row's 128 scores of a key tile come from TMEM into
+//                   registers at once, so maxima and sums need no exchange;
+//   warp 8          TMA: Q tiles, then K and V tiles of 128 keys (V as it
+//                   lies, keys by dims: the MN-major B operand of P V);
+//   warps 9, 10     MMA, one issuer a tile: S = Q K^T and O += P V, P from
+//                   TMEM.
+// Heads up to 64 dims: S, P and O of both tiles lie side by side in TMEM and
+// S of the next key tile is computed during the softmax of this one.  Heads
+// up to 128: P takes the place of S, whose product is issued behind P V.
+// O is rescaled only when a row's maximum grew by more than 2^8 (P stays <=
+// 256, the division by the row sum makes it exact again).
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescale = 8.0f;
+constexpr int kBlockBytes = 128 * 128;  // [128 rows x 64 dims] of 16 bits
+
+// Score transforms of a kernel instance.
+constexpr int kCap = 1, kBias = 2;
+
+template <int NB>  // 64-dim blocks of a head: 1 or 2
+struct TileCfg {
+  static constexpr int kStages = NB == 1 ? 4 : 2;
+  static constexpr int kQBufs = NB == 1 ? 2 : 1;
+  static constexpr int kTileBytes = NB * kBlockBytes;
+  static constexpr int kOffQ = 0;  // [buffer][tile]
+  static constexpr int kOffK = kOffQ + kQBufs * 2 * kTileBytes;
+  static constexpr int kOffV = kOffK + kStages * kTileBytes;
+  static constexpr int kSmem = kOffV + kStages * kTileBytes + 1024;
+  static constexpr bool kAliasP = NB == 2;
+  static constexpr uint32_t kColS = 0, kColO = 256, kColP = NB == 1 ? 384 : 0;
+  static constexpr uint32_t kStepO = 64 * NB, kStepP = NB == 1 ? 64 : 128;
+};
+// Three warpgroups; the softmax ones take registers from the third: 2 * 128 *
+// 208 + 128 * 88 = 384 * 168, what the launch gives.
+constexpr int kTileThreads = 12 * 32;
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;
+
+struct TileParams {
+  MaskedAttnParams a;
+  int n_pairs, n_items;        // 256-row groups of a head; items = B * hq * n_pairs
+  int q_step, k_step, v_step;  // bit 0: batch, bit 1: token, bit 2: head axis has a stride (0: broadcast)
+};
+
+// The key tiles of one item: tile j holds keys lo + 128 j ..; query tile g
+// needs tiles [first[g], last[g]).
+struct Item {
+  int b, h, q0, lo, hi, n, first[2], last[2];
+};
+
+__device__ __forceinline__ Item load_item(const TileParams& p, int idx, int lane) {
+  const MaskedAttnParams& a = p.a;
+  Item it;
+  const int bh_all = a.B * a.hq;
+  int pair, bh;
+  if (a.causal) {  // the longest rows of every head first
+    pair = p.n_pairs - 1 - idx / bh_all;
+    bh = idx % bh_all;
+  } else {         // neighbours share a head's keys
+    bh = idx / p.n_pairs;
+    pair = idx - bh * p.n_pairs;
+  }
+  it.b = bh / a.hq;
+  it.h = bh - it.b * a.hq;
+  it.q0 = pair * 256;
+  // lanes 0..3: first key of tile 0's first row, end of its last row, the same of tile 1
+  int v = 0;
+  const int g = (lane >> 1) & 1;
+  int r0 = it.q0 + 128 * g, r1 = min(r0 + 128, a.Nq) - 1;
+  if (a.n_docs > 0) {
+    const int* off = a.doc_offsets + static_cast<long long>(it.b) * (a.n_docs + 1);
+    r0 = max(r0, __ldg(off));
+    r1 = min(r1, __ldg(off + a.n_docs) - 1);
+  }
+  if (lane < 4 && r0 <= r1) {
+    const RowKeys r = row_keys(a, it.b, (lane & 1) ? r1 : r0);
+    v = (lane & 1) ? r.hi : r.lo;
+  }
+  int lo[2], hi[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    lo[t] = __shfl_sync(0xffffffffu, v, 2 * t);
+    hi[t] = __shfl_sync(0xffffffffu, v, 2 * t + 1);
+  }
+  const bool any0 = hi[0] > lo[0], any1 = hi[1] > lo[1];
+  it.lo = any0 ? (any1 ? min(lo[0], lo[1]) : lo[0]) : lo[1];
+  it.hi = max(any0 ? hi[0] : 0, any1 ? hi[1] : 0);
+  it.n = any0 || any1 ? (it.hi - it.lo + 127) >> 7 : 0;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const bool any = t ? any1 : any0;
+    it.first[t] = any ? (lo[t] - it.lo) >> 7 : 0;
+    it.last[t] = any ? (hi[t] - it.lo + 127) >> 7 : 0;
+  }
+  return it;
+}
+
+// tanh(z) = z P(z^2) for |z| <= 1; P by weighted least squares driven to equal
+// ripple (softmax_fit.py): relative error 6.9e-6 with 5 terms (bf16
+// probabilities), 5.9e-7 with 6.
+template <bool BF>
+struct TanhPoly;
+template <>
+struct TanhPoly<true> {
+  static constexpr int kTerms = 5;
+  static __device__ __forceinline__ float c(int k) {
+    constexpr float v[5] = {0.999993089590493f, -0.3329806545269403f, 0.13036811735219106f, -0.04481755800903122f,
+                            0.009036424468049704f};
+    return v[k];
+  }
+};
+template <>
+struct TanhPoly<false> {
+  static constexpr int kTerms = 6;
+  static __device__ __forceinline__ float c(int k) {
+    constexpr float v[6] = {0.9999994136209384f, -0.3332904241225214f, 0.13281434020653068f,
+                            -0.051605676150095f, 0.016743116205360516f, -0.0030670603865920864f};
+    return v[k];
+  }
+};
+
+// s[] (raw dot products) to scores in the exp2 domain, for the instances
+// whose scores are more than a multiple of the dot product.
+template <int MODE, bool BF>
+__device__ __forceinline__ void transform_scores(const MaskedAttnParams& p, float (&s)[128], float c, float slope2,
+                                                 float dist0) {
+  if constexpr ((MODE & kCap) != 0) {
+    // cap * log2 e * tanh(z), z = s * scale / cap: the polynomial where every
+    // |z| of the warp's rows is at most 1, else 1 - 2 / (1 + e^2z)
+    const float zs = p.scale / p.cap, kl = p.cap * kLog2e;
+    float big[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 128; e += 8) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) big[t] = fmax3(big[t], fabsf(s[e + t]), fabsf(s[e + 4 + t]));
+    }
+    const float top = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * fabsf(zs);
+    if (__all_sync(0xffffffffu, top <= 1.0f)) {
+      using T = TanhPoly<BF>;
+      uint64_t q[T::kTerms];
+#pragma unroll
+      for (int k = 0; k < T::kTerms; ++k) q[k] = f2_pack(T::c(k) * kl, T::c(k) * kl);
+      const uint64_t zs2 = f2_pack(zs, zs);
+#pragma unroll
+      for (int e = 0; e < 128; e += 2) {
+        const uint64_t z = f2_mul(f2_pack(s[e], s[e + 1]), zs2);
+        const uint64_t t = f2_mul(z, z);
+        uint64_t y = q[T::kTerms - 1];
+#pragma unroll
+        for (int k = T::kTerms - 2; k >= 0; --k) y = f2_fma(y, t, q[k]);
+        f2_unpack(f2_mul(y, z), s[e], s[e + 1]);
+      }
+    } else {
+      const float z2 = 2.0f * kLog2e * zs;
+#pragma unroll
+      for (int e = 0; e < 128; ++e) {
+        const float w = ex2_approx(s[e] * z2);
+        s[e] = fmaf(-2.0f * kl, rcp_approx(1.0f + w), kl);
+      }
+    }
+  }
+  if constexpr ((MODE & kBias) != 0) {
+    // slope * |p - j| as the magnitude of slope * (p - j), with the sign of -slope
+    const uint32_t sign = slope2 > 0.f ? 0x80000000u : 0u;
+    const float b0 = slope2 * dist0;
+#pragma unroll
+    for (int e = 0; e < 128; ++e) {
+      const float t = fmaf(-slope2, static_cast<float>(e), b0);
+      const float bias = __uint_as_float((__float_as_uint(t) & 0x7fffffffu) | sign);
+      s[e] = (MODE & kCap) ? s[e] + bias : fmaf(s[e], c, bias);
+    }
+  }
+}
+
+}  // namespace
+
+template <int NB, bool BF, int MODE>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    masked_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TileParams p) {
+  using C = TileCfg<NB>;
+  constexpr int kStages = C::kStages, kQBufs = C::kQBufs;
+  extern __shared__ uint8_t dsmem[];
+  __shared__ uint64_t q_full[kQBufs][2], q_empty[kQBufs][2];
+  __shared__ uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  __shared__ uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], drain_bar[2];
+  __shared__ uint32_t tmem_sh;
+  __shared__ int abort_sh;
+
+  const uint32_t raw = smem_u32(dsmem);
+  uint8_t* sm = dsmem + ((1024u - (raw & 1023u)) & 1023u);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const MaskedAttnParams& a = p.a;
+
+  if (threadIdx.x == 0) {
+    for (int g = 0; g < 2; ++g) {
+      for (int i = 0; i < kQBufs; ++i) {
+        mbar_init(&q_full[i][g], 1);
+        mbar_init(&q_empty[i][g], 1);
+      }
+      mbar_init(&s_full[g], 1);
+      mbar_init(&s_free[g], 128);
+      mbar_init(&p_full[g], 128);
+      mbar_init(&pv_done[g], 1);
+      mbar_init(&drain_bar[g], 1);
+    }
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 2);  // one release per issuer
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 2);
+    }
+    abort_sh = 0;
+    mbar_fence_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(&tmem_sh, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_sh;
+  pdl_wait();
+  pdl_trigger();
+
+  WaitCtl w;
+  w.abort = reinterpret_cast<volatile int*>(&abort_sh);
+  w.err = &g_masked_err;
+  w.timeout_ns = a.timeout_ns;
+  w.where = (KID_ATTN << 8) | static_cast<unsigned>(warp);
+
+  if (warp >= 8) {
+  regs_lower<kRegsOther>();
+  if (warp == 8) {
+    // ---------------------------------------------------------------- TMA
+    bool ok = true;
+    uint32_t kv = 0;             // key tiles loaded so far
+    uint32_t qc[2] = {0, 0};     // Q tiles loaded so far
+    uint32_t karmed = 0, varmed = 0;
+    for (int idx = blockIdx.x; ok && idx < p.n_items; idx += gridDim.x) {
+      const Item it = load_item(p, idx, lane);
+      if (lane == 0) {
+        const int hk = it.h / (a.hq / a.hk);
+        const int qb = (p.q_step & 1) ? it.b : 0, qh = (p.q_step & 4) ? it.h : 0;
+        const int kb = (p.k_step & 1) ? it.b : 0, kh = (p.k_step & 4) ? hk : 0;
+        const int vb = (p.v_step & 1) ? it.b : 0, vh = (p.v_step & 4) ? hk : 0;
+        for (int g = 0; ok && g < 2; ++g) {
+          if (it.last[g] == 0) continue;
+          const int buf = static_cast<int>(qc[g] % kQBufs);
+          if (!mbar_wait(&q_empty[buf][g], ((qc[g] / kQBufs) & 1) ^ 1, w)) {
+            ok = false;
+            break;
+          }
+          mbar_expect_tx(&q_full[buf][g], C::kTileBytes);
+          for (int c = 0; c < NB; ++c)
+            tma_load_4d(sm + C::kOffQ + (buf * 2 + g) * C::kTileBytes + c * kBlockBytes, &tmQ, &q_full[buf][g], 64 * c,
+                        qh, it.q0 + 128 * g, qb);
+          ++qc[g];
+        }
+        for (int j = 0; ok && j < it.n; ++j, ++kv) {
+          const int s = static_cast<int>(kv % kStages);
+          const uint32_t ph = (kv / kStages) & 1;
+          const int key = it.lo + 128 * j;
+          if (!mbar_wait(&k_empty[s], ph ^ 1, w)) {
+            ok = false;
+            break;
+          }
+          mbar_expect_tx(&k_full[s], C::kTileBytes);
+          for (int c = 0; c < NB; ++c)
+            tma_load_4d(sm + C::kOffK + s * C::kTileBytes + c * kBlockBytes, &tmK, &k_full[s], 64 * c, kh, key, kb);
+          karmed = (karmed & ~(3u << (2 * s))) | ((1u | (ph << 1)) << (2 * s));
+          if (!mbar_wait(&v_empty[s], ph ^ 1, w)) {
+            ok = false;
+            break;
+          }
+          mbar_expect_tx(&v_full[s], C::kTileBytes);
+          for (int c = 0; c < NB; ++c)
+            tma_load_4d(sm + C::kOffV + s * C::kTileBytes + c * kBlockBytes, &tmV, &v_full[s], 64 * c, vh, key, vb);
+          varmed = (varmed & ~(3u << (2 * s))) | ((1u | (ph << 1)) << (2 * s));
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    if (lane == 0) {  // whatever happened to the readers: the copies issued land before the CTA exits
+      for (int g = 0; g < 2; ++g)
+        for (uint32_t i = 0; i < kQBufs; ++i)
+          if (qc[g] > i) {
+            const uint32_t last = qc[g] - 1 - i;
+            mbar_wait_drain(&q_full[last % kQBufs][g], (last / kQBufs) & 1);
+          }
+      for (int s = 0; s < kStages; ++s) {
+        if ((karmed >> (2 * s)) & 1u) mbar_wait_drain(&k_full[s], (karmed >> (2 * s + 1)) & 1u);
+        if ((varmed >> (2 * s)) & 1u) mbar_wait_drain(&v_full[s], (varmed >> (2 * s + 1)) & 1u);
+      }
+    }
+  } else if (warp == 9 || warp == 10) {
+    // ---------------------------------------------------------------- MMA
+    const int g = warp - 9;
+    const uint32_t idesc_s = idesc_f16_f32(128, 128, BF);
+    const int dv = (a.d + 15) & ~15;  // dims of the products: zeros behind d
+    const uint32_t idesc_o = idesc_f16_f32(128, dv, BF) | kIdescBMnMajor;
+    const uint32_t tS = tmem + C::kColS + 128 * g, tO = tmem + C::kColO + C::kStepO * g,
+                   tP = tmem + C::kColP + C::kStepP * g;
+    bool ok = true;
+    uint32_t kc = 0, vc = 0, qc = 0, sc = 0, pc = 0;  // K, V, Q tiles seen, S and PV products issued
+    for (int idx = blockIdx.x; ok && idx < p.n_items; idx += gridDim.x) {
+      const Item it = load_item(p, idx, lane);
+      if (lane == 0 && it.n > 0) {
+        const int first = it.first[g], last = it.last[g];
+        const int buf = static_cast<int>(qc % kQBufs);
+        if (last > 0) {
+          ok = mbar_wait(&q_full[buf][g], (qc / kQBufs) & 1, w);
+          ++qc;
+        }
+        const uint32_t qa = smem_u32(sm + C::kOffQ + (buf * 2 + g) * C::kTileBytes);
+        // step j: S of tile j; P V of tile j, or (P beside S) of tile j - 1
+        constexpr int kLag = C::kAliasP ? 0 : 1;
+        for (int j = 0; ok && j < it.n + kLag; ++j) {
+          if (j < it.n) {
+            const int ks = static_cast<int>(kc % kStages);
+            if (!mbar_wait(&k_full[ks], (kc / kStages) & 1, w)) {
+              ok = false;
+              break;
+            }
+            ++kc;
+            if (j >= first && j < last) {
+              // P beside S: S may be overwritten once the softmax has taken the tile
+              // before; P in S's place: the product that reads it was issued before
+              if (!C::kAliasP && sc > 0 && !mbar_wait(&s_free[g], (sc - 1) & 1, w)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t ka = smem_u32(sm + C::kOffK + ks * C::kTileBytes);
+              for (int t = 0; t < dv / 16; ++t) {
+                const uint32_t off = (t >> 2) * kBlockBytes + (t & 3) * 32;
+                tc_mma_f16_ss(tS, sdesc_kmajor_sw128(qa + off), sdesc_kmajor_sw128(ka + off), idesc_s, t > 0 ? 1u : 0u);
+              }
+              tc_commit(&s_full[g]);
+              ++sc;
+              if (j == last - 1) tc_commit(&q_empty[buf][g]);
+              tc_commit(&k_empty[ks]);
+            } else {
+              mbar_arrive(&k_empty[ks]);
+            }
+          }
+          const int jv = j - kLag;
+          if (jv >= 0) {
+            const int vs = static_cast<int>(vc % kStages);
+            if (!mbar_wait(&v_full[vs], (vc / kStages) & 1, w)) {
+              ok = false;
+              break;
+            }
+            ++vc;
+            if (jv >= first && jv < last) {
+              if (!mbar_wait(&p_full[g], pc & 1, w)) {
+                ok = false;
+                break;
+              }
+              ++pc;
+              tc_fence_after();
+              const uint32_t va = smem_u32(sm + C::kOffV + vs * C::kTileBytes);
+#pragma unroll
+              for (int t = 0; t < 8; ++t)  // 16 keys each
+                tc_mma_f16_ts(tO, tP + 8 * t, sdesc_mnmajor_sw128(va + t * 2048, kBlockBytes), idesc_o,
+                              (jv > first || t > 0) ? 1u : 0u);
+              tc_commit(&pv_done[g]);
+              tc_commit(&v_empty[vs]);
+            } else {
+              mbar_arrive(&v_empty[vs]);
+            }
+          }
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    if (lane == 0) {
+      tc_commit(&drain_bar[g]);
+      mbar_wait_drain(&drain_bar[g], 0);
+    }
+  }
+  } else {
+    regs_raise<kRegsSoftmax>();
+    // ------------------------------------------------------------ softmax
+    const int g = warp >> 2, quad = warp & 3;
+    const int r = quad * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t tS = tmem + C::kColS + 128 * g + lane_off, tO = tmem + C::kColO + C::kStepO * g + lane_off,
+                   tP = tmem + C::kColP + C::kStepP * g + lane_off;
+    const float c = a.scale * kLog2e;
+    bool ok = true;
+    uint32_t cnt = 0, kv = 0;  // this tile's key tiles so far, the CTA's
+    for (int idx = blockIdx.x; ok && idx < p.n_items; idx += gridDim.x) {
+      const Item it = load_item(p, idx, lane);
+      const int i = it.q0 + 128 * g + r;
+      const bool row = i < a.Nq;
+      RowKeys rk;
+      rk.lo = rk.hi = rk.pos = 0;
+      rk.written = false;
+      if (row) rk = row_keys(a, it.b, i);
+      const float slope2 = (MODE & kBias) && a.slopes ? __ldg(a.slopes + it.h) * kLog2e : 0.f;
+      const int first = it.first[g], last = it.last[g];
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int j = first; j < last; ++j, ++cnt) {
+        const int base = it.lo + 128 * j;
+        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[g], cnt & 1, w))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float s[128];
+        {
+          uint32_t u[64], v[64];
+          tmem_ld64(tS, u);
+          tmem_ld64(tS + 64, v);
+#pragma unroll
+          for (int e = 0; e < 64; ++e) {
+            s[e] = __uint_as_float(u[e]);
+            s[64 + e] = __uint_as_float(v[e]);
+          }
+        }
+        if (!C::kAliasP) {
+          tc_fence_before();
+          mbar_arrive(&s_free[g]);
+        }
+        if constexpr (MODE != 0)
+          transform_scores<MODE, BF>(a, s, c, slope2, static_cast<float>(static_cast<long long>(rk.pos) - base));
+        const int rlo = rk.lo - base, rhi = rk.hi - base;
+        if (!__all_sync(0xffffffffu, rlo <= 0 && rhi >= 128)) {
+#pragma unroll
+          for (int e = 0; e < 128; ++e) s[e] = (e >= rlo && e < rhi) ? s[e] : -INFINITY;
+        }
+        float mx[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) mx[t] = fmax3(s[t], s[4 + t], s[8 + t]);
+#pragma unroll
+        for (int e = 12; e < 124; e += 8) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t) mx[t] = fmax3(mx[t], s[e + t], s[e + 4 + t]);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) mx[t] = fmaxf(mx[t], s[124 + t]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const float m_new = fmaxf(m_run, MODE == 0 ? top * c : top);
+        const bool grow = m_new > m_run + kRescale;
+        const float alpha = grow ? ex2_approx(m_run - m_new) : 1.0f;  // exp2(-inf) = 0 on the first tile
+        l_run *= alpha;
+        if (grow) m_run = m_new;
+        // a row that has seen no allowed key yet keeps m = -inf: all its p are 0
+        const float m_use = m_run == -INFINITY ? 0.0f : m_run;
+        if (j > first) {
+          // O is stable (and, beside S, P free) once the product of the tile before is done
+          if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[g], (cnt - 1) & 1, w))) {
+            ok = false;
+            break;
+          }
+          if (__any_sync(0xffffffffu, grow)) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int t = 0; t < a.d; t += 16) {
+              uint32_t o[16];
+              tmem_ld16(tO + t, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st16(tO + t, o);
+            }
+          }
+        }
+        const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(-m_use, -m_use);
+        uint64_t sum2[2] = {0ull, 0ull};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const uint64_t v = f2_pack(s[32 * q + 2 * e], s[32 * q + 2 * e + 1]);
+            float xa, xb;
+            f2_unpack(MODE == 0 ? f2_fma(v, c2, nm2) : f2_add(v, nm2), xa, xb);
+            const float pa = ex2_approx(xa), pb = ex2_approx(xb);
+            sum2[e & 1] = f2_add(sum2[e & 1], f2_pack(pa, pb));
+            pk[e] = pack2<BF>(pa, pb);
+          }
+          tmem_st16_nowait(tP + 16 * q, pk);
+        }
+        tmem_wait_st();
+        float sa, sb;
+        f2_unpack(f2_add(sum2[0], sum2[1]), sa, sb);
+        l_run += sa + sb;
+        if (j == it.n - 1 && it.hi - base < 128 && it.hi < a.Nk) {
+          // values behind the last key that any row reads: zeros, since P's
+          // zeros would not hide a NaN or an infinity there
+          const uint32_t t = kv + static_cast<uint32_t>(j);
+          if (!__all_sync(0xffffffffu, mbar_wait(&v_full[t % kStages], (t / kStages) & 1, w))) {
+            ok = false;
+            break;
+          }
+          if (r >= it.hi - base) {
+            const uint32_t at = smem_u32(sm + C::kOffV + (t % kStages) * C::kTileBytes) + r * 128;
+            for (int x = 0; x < NB * 8; ++x) st_shared_v4(at + (x >> 3) * kBlockBytes + (x & 7) * 16, 0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        mbar_arrive(&p_full[g]);
+      }
+      kv += static_cast<uint32_t>(it.n);
+      if (!ok) break;
+      const bool some = last > first;
+      if (some && !__all_sync(0xffffffffu, mbar_wait(&pv_done[g], (cnt - 1) & 1, w))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const bool full_row = rk.hi > rk.lo;
+      const float inv = full_row ? 1.0f / l_run : 0.f;
+      uint16_t* dst = a.out + it.b * a.o_b + static_cast<long long>(i) * a.o_n + it.h * a.o_h;
+      float odd = 0.f;  // 0 unless a value of the row is not finite
+#pragma unroll 1
+      for (int t = 0; t < a.d; t += 16) {
+        uint32_t o[16];
+        if (some) tmem_ld16(tO + t, o);
+        uint32_t h[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = some && full_row ? __uint_as_float(o[2 * e]) * inv : 0.f;
+          const float y = some && full_row ? __uint_as_float(o[2 * e + 1]) * inv : 0.f;
+          odd = fmaf(x, 0.f, fmaf(y, 0.f, odd));
+          h[e] = pack2<BF>(x, y);
+        }
+        if (row && rk.written) {
+          *reinterpret_cast<uint4*>(dst + t) = make_uint4(h[0], h[1], h[2], h[3]);
+          if (t + 8 < a.d) *reinterpret_cast<uint4*>(dst + t + 8) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+      }
+      // A value that is not finite may have come from a key that the row does
+      // not read (0 * inf in the tile's product): such rows anew, by the
+      // definition.
+      unsigned again = __ballot_sync(0xffffffffu, row && rk.written && full_row && !(odd == 0.f));
+      while (again) {
+        const int src = __ffs(again) - 1;
+        again &= again - 1;
+        RowKeys o;
+        o.lo = __shfl_sync(0xffffffffu, rk.lo, src);
+        o.hi = __shfl_sync(0xffffffffu, rk.hi, src);
+        o.pos = __shfl_sync(0xffffffffu, rk.pos, src);
+        o.written = true;
+        attend_row<BF>(a, it.b, it.q0 + 128 * g + quad * 32 + src, it.h, o, lane);
+      }
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem_sh, 512);
+  }
+}
+
+namespace {
+
+// [B, N, heads, d] as a map of (d, heads, N, B) with tiles of 128 tokens by 64
+// dims, zeros outside; an axis without a stride has length 1.  Returns the
+// axes that have one (TileParams::q_step).
+bool make_tile_map(CUtensorMap* m, const uint16_t* data, int d, int H, int N, int B, long long sh, long long sn,
+                   long long sb, int* step) {
+  const bool hb = B > 1 && sb > 0, hh = H > 1 && sh > 0, hn = N > 1 && sn > 0;
+  if (N > 1 && !hn) return false;
+  const uint64_t dims[4] = {static_cast<uint64_t>(d), hh ? static_cast<uint64_t>(H) : 1u, static_cast<uint64_t>(N),
+                            hb ? static_cast<uint64_t>(B) : 1u};
+  const uint64_t one = static_cast<uint64_t>(d) * 2;
+  const uint64_t str[3] = {hh ? static_cast<uint64_t>(sh) * 2 : one, hn ? static_cast<uint64_t>(sn) * 2 : one,
+                           hb ? static_cast<uint64_t>(sb) * 2 : one};
+  const uint32_t box[4] = {64, 1, 128, 1};
+  *step = (hb ? 1 : 0) | (hn ? 2 : 0) | (hh ? 4 : 0);
+  return make_tmap_f16(m, data, 4, dims, str, box);
+}
+
+template <int NB, bool BF, int MODE>
+int launch_tiles(const TileParams& p, const CUtensorMap* tm, cudaStream_t st) {
+  using C = TileCfg<NB>;
+  auto kern = masked_tiles_kernel<NB, BF, MODE>;
+  static std::atomic<unsigned long long> attr_done{0};
+  if (!smem_attr_once(attr_done, kern, C::kSmem)) return JEPA_B200_ERR_CUDA;
+  const int grid = p.n_items < num_sms() ? p.n_items : num_sms();
+  return launch_pdl(kern, dim3(grid), dim3(kTileThreads), C::kSmem, st, 1, tm[0], tm[1], tm[2], p) == cudaSuccess
+             ? JEPA_B200_OK
+             : JEPA_B200_ERR_CUDA;
+}
+
+template <int NB, bool BF>
+int launch_tiles_mode(const TileParams& p, const CUtensorMap* tm, cudaStream_t st) {
+  // a scale that is not positive turns maxima of dot products into minima:
+  // the instance that scales first
+  const int mode = (p.a.cap > 0.f ? kCap : 0) | (p.a.slopes || !(p.a.scale > 0.f || p.a.cap > 0.f) ? kBias : 0);
+  switch (mode) {
+    case 0: return launch_tiles<NB, BF, 0>(p, tm, st);
+    case kCap: return launch_tiles<NB, BF, kCap>(p, tm, st);
+    case kBias: return launch_tiles<NB, BF, kBias>(p, tm, st);
+    default: return launch_tiles<NB, BF, kCap | kBias>(p, tm, st);
+  }
+}
+
+}  // namespace
+
 int masked_attention_take_error(unsigned* code) {
   DevErr h{0, 0};
   if (cudaMemcpyFromSymbol(&h, g_masked_err, sizeof(h)) != cudaSuccess) return JEPA_B200_ERR_CUDA;
@@ -152,6 +762,21 @@ int masked_attention_take_error(unsigned* code) {
 }
 
 int launch_masked_attention(const MaskedAttnParams& p, bool bf16, cudaStream_t st) {
+  if (p.Nq > 16) {
+    TileParams tp;
+    tp.a = p;
+    tp.n_pairs = (p.Nq + 255) / 256;
+    const long long items = static_cast<long long>(p.B) * p.hq * tp.n_pairs;
+    if (items > 0x7fffffffll) return JEPA_B200_ERR_SHAPE;
+    tp.n_items = static_cast<int>(items);
+    CUtensorMap tm[3];
+    if (p.Nk > 0 && make_tile_map(&tm[0], p.q, p.d, p.hq, p.Nq, p.B, p.q_h, p.q_n, p.q_b, &tp.q_step) &&
+        make_tile_map(&tm[1], p.k, p.d, p.hk, p.Nk, p.B, p.k_h, p.k_n, p.k_b, &tp.k_step) &&
+        make_tile_map(&tm[2], p.v, p.d, p.hk, p.Nk, p.B, p.v_h, p.v_n, p.v_b, &tp.v_step)) {
+      if (p.d <= 64) return bf16 ? launch_tiles_mode<1, true>(tp, tm, st) : launch_tiles_mode<1, false>(tp, tm, st);
+      return bf16 ? launch_tiles_mode<2, true>(tp, tm, st) : launch_tiles_mode<2, false>(tp, tm, st);
+    }
+  }
   const long long rows = static_cast<long long>(p.B) * p.Nq * p.hq;
   const long long blocks = (rows + 3) / 4;
   if (blocks > 0x7fffffffll) return JEPA_B200_ERR_SHAPE;
