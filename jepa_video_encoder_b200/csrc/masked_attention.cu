@@ -178,9 +178,9 @@ struct TileCfg {
   static constexpr uint32_t kStepO = 64 * NB, kStepP = NB == 1 ? 64 : 128;
 };
 // Three warpgroups; the softmax ones take registers from the third: 2 * 128 *
-// 208 + 128 * 88 = 384 * 168, what the launch gives.
+// 224 + 128 * 56 = 384 * 168, what the launch gives.
 constexpr int kTileThreads = 12 * 32;
-constexpr int kRegsSoftmax = 208, kRegsOther = 88;
+constexpr int kRegsSoftmax = 224, kRegsOther = 56;
 
 struct TileParams {
   MaskedAttnParams a;
@@ -265,44 +265,59 @@ struct TanhPoly<false> {
   }
 };
 
-// s[] (raw dot products) to scores in the exp2 domain, for the instances
-// whose scores are more than a multiple of the dot product.
-template <int MODE, bool BF>
-__device__ __forceinline__ void transform_scores(const MaskedAttnParams& p, float (&s)[128], float c, float slope2,
-                                                 float dist0) {
-  if constexpr ((MODE & kCap) != 0) {
-    // cap * log2 e * tanh(z), z = s * scale / cap: the polynomial where every
-    // |z| of the warp's rows is at most 1, else 1 - 2 / (1 + e^2z)
-    const float zs = p.scale / p.cap, kl = p.cap * kLog2e;
-    float big[4] = {0.f, 0.f, 0.f, 0.f};
+// How the exponent of a score is made from its register: s * c - m of a raw
+// dot product, s - m of a finished score, or the capped score of a raw dot
+// product by its polynomial, s * Q(s^2) - m.
+enum { FROM_DOT = 0, FROM_SCORE = 1, FROM_CAP = 2 };
+
+// Coefficients of cap * log2 e * tanh(s scale / cap) = s Q(s^2) as a
+// polynomial in s^2, and whether it serves: every |s scale / cap| at most 1,
+// no coefficient out of f32's range.
+template <bool BF>
+struct CapPoly {
+  uint64_t q[TanhPoly<BF>::kTerms];
+  float zs, kl;  // scale / cap, cap * log2 e
+  bool usable;
+  __device__ __forceinline__ void init(float scale, float cap) {
+    zs = scale / cap;
+    kl = cap * kLog2e;
+    usable = fabsf(zs) > 2e-4f && fabsf(zs) < 1e3f && kl < 1e6f;
+    float f = kl * zs;
 #pragma unroll
-    for (int e = 0; e < 128; e += 8) {
-#pragma unroll
-      for (int t = 0; t < 4; ++t) big[t] = fmax3(big[t], fabsf(s[e + t]), fabsf(s[e + 4 + t]));
+    for (int k = 0; k < TanhPoly<BF>::kTerms; ++k) {
+      q[k] = f2_pack(TanhPoly<BF>::c(k) * f, TanhPoly<BF>::c(k) * f);
+      f *= zs * zs;
     }
-    const float top = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * fabsf(zs);
-    if (__all_sync(0xffffffffu, top <= 1.0f)) {
-      using T = TanhPoly<BF>;
-      uint64_t q[T::kTerms];
+  }
+  __device__ __forceinline__ bool fits(float big) const { return usable && big * fabsf(zs) <= 1.0f; }
+  // Q(s^2) of two scores
+  __device__ __forceinline__ uint64_t slope(uint64_t s) const {
+    const uint64_t t = f2_mul(s, s);
+    uint64_t y = q[TanhPoly<BF>::kTerms - 1];
 #pragma unroll
-      for (int k = 0; k < T::kTerms; ++k) q[k] = f2_pack(T::c(k) * kl, T::c(k) * kl);
-      const uint64_t zs2 = f2_pack(zs, zs);
+    for (int k = TanhPoly<BF>::kTerms - 2; k >= 0; --k) y = f2_fma(y, t, q[k]);
+    return y;
+  }
+  // any score: kl (1 - 2 / (1 + e^2z))
+  __device__ __forceinline__ float exact(float s) const {
+    return fmaf(-2.0f * kl, rcp_approx(1.0f + ex2_approx(s * (2.0f * kLog2e * zs))), kl);
+  }
+};
+
+// Raw dot products in s[] to scores in the exp2 domain.
+template <int MODE, bool BF>
+__device__ __forceinline__ void finish_scores(float (&s)[128], const CapPoly<BF>& cap, bool poly, float c, float slope2,
+                                              float dist0) {
+  if constexpr ((MODE & kCap) != 0) {
+    if (poly) {
 #pragma unroll
       for (int e = 0; e < 128; e += 2) {
-        const uint64_t z = f2_mul(f2_pack(s[e], s[e + 1]), zs2);
-        const uint64_t t = f2_mul(z, z);
-        uint64_t y = q[T::kTerms - 1];
-#pragma unroll
-        for (int k = T::kTerms - 2; k >= 0; --k) y = f2_fma(y, t, q[k]);
-        f2_unpack(f2_mul(y, z), s[e], s[e + 1]);
+        const uint64_t v = f2_pack(s[e], s[e + 1]);
+        f2_unpack(f2_mul(v, cap.slope(v)), s[e], s[e + 1]);
       }
     } else {
-      const float z2 = 2.0f * kLog2e * zs;
 #pragma unroll
-      for (int e = 0; e < 128; ++e) {
-        const float w = ex2_approx(s[e] * z2);
-        s[e] = fmaf(-2.0f * kl, rcp_approx(1.0f + w), kl);
-      }
+      for (int e = 0; e < 128; ++e) s[e] = cap.exact(s[e]);
     }
   }
   if constexpr ((MODE & kBias) != 0) {
@@ -315,8 +330,120 @@ __device__ __forceinline__ void transform_scores(const MaskedAttnParams& p, floa
       const float bias = __uint_as_float((__float_as_uint(t) & 0x7fffffffu) | sign);
       s[e] = (MODE & kCap) ? s[e] + bias : fmaf(s[e], c, bias);
     }
+  } else if constexpr (MODE == 0) {
+#pragma unroll
+    for (int e = 0; e < 128; ++e) s[e] *= c;
   }
 }
+
+// 2^x of two arguments without the special-function unit (Cody and Waite's
+// reduction: x = n + f, n the nearest integer, taken from the low bits of x +
+// 1.5 * 2^23; a polynomial on [-1/2, 1/2], least squares driven to equal
+// ripple, softmax_fit.py: relative error 7.5e-5 of degree 3 for bf16
+// probabilities, 2.6e-6 of degree 4 for f16; n added to the exponent).
+// Arguments below -126 give 2^-126.  A NaN does not come out as a NaN but as
+// a value that overflows the 16-bit type.
+template <bool BF>
+__device__ __forceinline__ void ex2_poly2(uint64_t x, float& pa, float& pb) {
+  constexpr float kMagic = 12582912.0f;
+  float xa, xb;
+  f2_unpack(x, xa, xb);
+  x = f2_pack(max_nan(xa, -126.0f), max_nan(xb, -126.0f));
+  const uint64_t t = f2_add(x, f2_pack(kMagic, kMagic));
+  const uint64_t f = f2_fma(f2_add(t, f2_pack(-kMagic, -kMagic)), f2_pack(-1.0f, -1.0f), x);
+  uint64_t y;
+  if constexpr (BF) {
+    y = f2_fma(f, f2_pack(0.055171669359523244f, 0.055171669359523244f), f2_pack(0.24261113138277252f, 0.24261113138277252f));
+    y = f2_fma(y, f, f2_pack(0.6932609862029608f, 0.6932609862029608f));
+    y = f2_fma(y, f, f2_pack(0.9999280729973522f, 0.9999280729973522f));
+  } else {
+    y = f2_fma(f, f2_pack(0.009570101946824233f, 0.009570101946824233f), f2_pack(0.055917861585536834f, 0.055917861585536834f));
+    y = f2_fma(y, f, f2_pack(0.24024744837984294f, 0.24024744837984294f));
+    y = f2_fma(y, f, f2_pack(0.6931218145829672f, 0.6931218145829672f));
+    y = f2_fma(y, f, f2_pack(0.9999992614392345f, 0.9999992614392345f));
+  }
+  float ya, yb, ta, tb;
+  f2_unpack(y, ya, yb);
+  f2_unpack(t, ta, tb);
+  pa = __uint_as_float(__float_as_uint(ya) + (__float_as_uint(ta) << 23));
+  pb = __uint_as_float(__float_as_uint(yb) + (__float_as_uint(tb) << 23));
+}
+
+// Largest of s[A..B) and of `top`, in four chains; of the magnitudes with ABS.
+template <int A, int B, bool ABS = false>
+__device__ __forceinline__ float row_max(const float (&s)[128], float top) {
+  const auto v = [&](int e) { return ABS ? fabsf(s[e]) : s[e]; };
+  float mx[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) mx[t] = fmaxf(v(A + t), v(A + 4 + t));
+#pragma unroll
+  for (int e = A + 8; e < B; e += 8) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) mx[t] = fmax3(mx[t], v(e + t), v(e + 4 + t));
+  }
+  return fmaxf(fmax3(mx[0], mx[1], mx[2]), fmaxf(mx[3], top));
+}
+
+// P of the tile's 128 keys into TMEM (two to a word), and their sum: one
+// straight run of code, so that exponentials of either kind overlap.
+template <int KIND, int POLY, bool BF>
+__device__ __forceinline__ float exp_tile(const float (&s)[128], uint64_t c2, uint64_t nm2, const CapPoly<BF>& cap,
+                                          uint32_t tP) {
+  uint64_t sum2[2] = {0ull, 0ull};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const uint64_t v = f2_pack(s[32 * q + 2 * e], s[32 * q + 2 * e + 1]);
+      const uint64_t x = KIND == FROM_DOT ? f2_fma(v, c2, nm2)
+                                          : (KIND == FROM_CAP ? f2_fma(v, cap.slope(v), nm2) : f2_add(v, nm2));
+      float pa, pb;
+      if ((e * POLY) % 16 + POLY < 16) {
+        f2_unpack(x, pa, pb);
+        pa = ex2_approx(pa);
+        pb = ex2_approx(pb);
+      } else {
+        ex2_poly2<BF>(x, pa, pb);
+      }
+      sum2[e & 1] = f2_add(sum2[e & 1], f2_pack(pa, pb));
+      pk[e] = pack2<BF>(pa, pb);
+    }
+    tmem_st16_nowait(tP + 16 * q, pk);
+  }
+  float sa, sb;
+  f2_unpack(f2_add(sum2[0], sum2[1]), sa, sb);
+  return sa + sb;
+}
+
+// mbar_wait whose thread sleeps; a bound of 0 gives up at once as there.
+constexpr uint32_t kSleepNs = 20000;
+__device__ __forceinline__ bool sleep_wait(uint64_t* bar, uint32_t parity, const WaitCtl& w) {
+  if (mbar_try_wait(bar, parity)) return true;
+  if (w.timeout_ns == 0) {
+    raise_error(w, DERR_TIMEOUT);
+    return false;
+  }
+  const unsigned long long t0 = globaltimer();
+  while (!mbar_try_wait_for(bar, parity, kSleepNs)) {
+    if (*w.abort) return false;
+    if (globaltimer() - t0 > w.timeout_ns) {
+      raise_error(w, DERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+// The same by a whole warp, its lanes together again behind it.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& w) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, sleep_wait(bar, parity, w));
+}
+
+// Pairs of every 16 whose exponential is the polynomial: the special-function
+// unit alone would be the bound.
+template <int MODE>
+constexpr int kPolyPairs = MODE == 0 ? 4 : (MODE == kBias ? 3 : 0);
 
 }  // namespace
 
@@ -345,17 +472,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         mbar_init(&q_empty[i][g], 1);
       }
       mbar_init(&s_full[g], 1);
-      mbar_init(&s_free[g], 128);
-      mbar_init(&p_full[g], 128);
+      mbar_init(&s_free[g], 4);  // one arrival a softmax warp
+      mbar_init(&p_full[g], 4);
       mbar_init(&pv_done[g], 1);
-      mbar_init(&drain_bar[g], 1);
     }
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&k_full[s], 1);
-      mbar_init(&k_empty[s], 2);  // one release per issuer
+      mbar_init(&k_empty[s], 1);
       mbar_init(&v_full[s], 1);
-      mbar_init(&v_empty[s], 2);
+      mbar_init(&v_empty[s], 1);
     }
+    mbar_init(&drain_bar[0], 1);
+    mbar_init(&drain_bar[1], 1);
     abort_sh = 0;
     mbar_fence_init();
   }
@@ -394,7 +522,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int g = 0; ok && g < 2; ++g) {
           if (it.last[g] == 0) continue;
           const int buf = static_cast<int>(qc[g] % kQBufs);
-          if (!mbar_wait(&q_empty[buf][g], ((qc[g] / kQBufs) & 1) ^ 1, w)) {
+          if (!sleep_wait(&q_empty[buf][g], ((qc[g] / kQBufs) & 1) ^ 1, w)) {
             ok = false;
             break;
           }
@@ -408,7 +536,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const int s = static_cast<int>(kv % kStages);
           const uint32_t ph = (kv / kStages) & 1;
           const int key = it.lo + 128 * j;
-          if (!mbar_wait(&k_empty[s], ph ^ 1, w)) {
+          if (!sleep_wait(&k_empty[s], ph ^ 1, w)) {
             ok = false;
             break;
           }
@@ -416,7 +544,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int c = 0; c < NB; ++c)
             tma_load_4d(sm + C::kOffK + s * C::kTileBytes + c * kBlockBytes, &tmK, &k_full[s], 64 * c, kh, key, kb);
           karmed = (karmed & ~(3u << (2 * s))) | ((1u | (ph << 1)) << (2 * s));
-          if (!mbar_wait(&v_empty[s], ph ^ 1, w)) {
+          if (!sleep_wait(&v_empty[s], ph ^ 1, w)) {
             ok = false;
             break;
           }
@@ -440,91 +568,118 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if ((varmed >> (2 * s)) & 1u) mbar_wait_drain(&v_full[s], (varmed >> (2 * s + 1)) & 1u);
       }
     }
-  } else if (warp == 9 || warp == 10) {
+  } else if (warp == 9 || (warp == 10 && !C::kAliasP)) {
     // ---------------------------------------------------------------- MMA
-    const int g = warp - 9;
+    // Both query tiles in a fixed turn: the tensor core works for one tile
+    // while the other is in its softmax.  P beside S: warp 9 issues S and warp
+    // 10 P V, each at its own pace.  P in S's place: warp 9 issues P V and the
+    // S that follows it, in order.  The whole warp walks
+    // the loop and one elected lane issues, on descriptors that differ by
+    // constants: operands then stay in uniform registers (a lane's own branch
+    // issues a 128 x 64 x 16 product every 60 to 104 clocks, this one every
+    // 32, the tensor core's own pace).
+    const bool lead = elect_one();
     const uint32_t idesc_s = idesc_f16_f32(128, 128, BF);
-    const int dv = (a.d + 15) & ~15;  // dims of the products: zeros behind d
-    const uint32_t idesc_o = idesc_f16_f32(128, dv, BF) | kIdescBMnMajor;
-    const uint32_t tS = tmem + C::kColS + 128 * g, tO = tmem + C::kColO + C::kStepO * g,
-                   tP = tmem + C::kColP + C::kStepP * g;
+    const int ksteps = (a.d + 15) >> 4;  // 16 dims each: zeros behind d
+    const uint32_t idesc_o = idesc_f16_f32(128, 16 * ksteps, BF) | kIdescBMnMajor;
+    const uint64_t qdesc = sdesc_kmajor_sw128(smem_u32(sm + C::kOffQ));
+    const uint64_t kdesc = sdesc_kmajor_sw128(smem_u32(sm + C::kOffK));
+    const uint64_t vdesc = sdesc_mnmajor_sw128(smem_u32(sm + C::kOffV), kBlockBytes);
+    constexpr uint64_t kTile16 = C::kTileBytes / 16, kBlock16 = kBlockBytes / 16;  // descriptors count 16 bytes
     bool ok = true;
-    uint32_t kc = 0, vc = 0, qc = 0, sc = 0, pc = 0;  // K, V, Q tiles seen, S and PV products issued
+    uint32_t ks = 0, kph = 0, vs = 0, vph = 0;        // stage and phase of the next K and V tile
+    uint32_t qc[2] = {0, 0}, sc[2] = {0, 0}, pc[2] = {0, 0};  // Q tiles, S and P V products so far
     for (int idx = blockIdx.x; ok && idx < p.n_items; idx += gridDim.x) {
       const Item it = load_item(p, idx, lane);
-      if (lane == 0 && it.n > 0) {
-        const int first = it.first[g], last = it.last[g];
-        const int buf = static_cast<int>(qc % kQBufs);
-        if (last > 0) {
-          ok = mbar_wait(&q_full[buf][g], (qc / kQBufs) & 1, w);
-          ++qc;
-        }
-        const uint32_t qa = smem_u32(sm + C::kOffQ + (buf * 2 + g) * C::kTileBytes);
-        // step j: S of tile j; P V of tile j, or (P beside S) of tile j - 1
-        constexpr int kLag = C::kAliasP ? 0 : 1;
-        for (int j = 0; ok && j < it.n + kLag; ++j) {
-          if (j < it.n) {
-            const int ks = static_cast<int>(kc % kStages);
-            if (!mbar_wait(&k_full[ks], (kc / kStages) & 1, w)) {
-              ok = false;
-              break;
-            }
-            ++kc;
-            if (j >= first && j < last) {
-              // P beside S: S may be overwritten once the softmax has taken the tile
-              // before; P in S's place: the product that reads it was issued before
-              if (!C::kAliasP && sc > 0 && !mbar_wait(&s_free[g], (sc - 1) & 1, w)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              const uint32_t ka = smem_u32(sm + C::kOffK + ks * C::kTileBytes);
-              for (int t = 0; t < dv / 16; ++t) {
-                const uint32_t off = (t >> 2) * kBlockBytes + (t & 3) * 32;
-                tc_mma_f16_ss(tS, sdesc_kmajor_sw128(qa + off), sdesc_kmajor_sw128(ka + off), idesc_s, t > 0 ? 1u : 0u);
-              }
-              tc_commit(&s_full[g]);
-              ++sc;
-              if (j == last - 1) tc_commit(&q_empty[buf][g]);
-              tc_commit(&k_empty[ks]);
-            } else {
-              mbar_arrive(&k_empty[ks]);
-            }
-          }
-          const int jv = j - kLag;
-          if (jv >= 0) {
-            const int vs = static_cast<int>(vc % kStages);
-            if (!mbar_wait(&v_full[vs], (vc / kStages) & 1, w)) {
-              ok = false;
-              break;
-            }
-            ++vc;
-            if (jv >= first && jv < last) {
-              if (!mbar_wait(&p_full[g], pc & 1, w)) {
-                ok = false;
-                break;
-              }
-              ++pc;
-              tc_fence_after();
-              const uint32_t va = smem_u32(sm + C::kOffV + vs * C::kTileBytes);
+      if (it.n == 0) continue;
+      uint32_t buf[2];
 #pragma unroll
-              for (int t = 0; t < 8; ++t)  // 16 keys each
-                tc_mma_f16_ts(tO, tP + 8 * t, sdesc_mnmajor_sw128(va + t * 2048, kBlockBytes), idesc_o,
-                              (jv > first || t > 0) ? 1u : 0u);
-              tc_commit(&pv_done[g]);
-              tc_commit(&v_empty[vs]);
-            } else {
-              mbar_arrive(&v_empty[vs]);
-            }
-          }
+      for (int g = 0; g < 2; ++g) {
+        buf[g] = qc[g] % kQBufs;
+        if (it.last[g] > 0 && warp == 9) {
+          ok = ok && warp_wait(&q_full[buf[g]][g], (qc[g] / kQBufs) & 1, w);
+          ++qc[g];
         }
       }
-      ok = __all_sync(0xffffffffu, ok);
+      // S of key tile j
+      const auto issue_s = [&](int j, int g) {
+        if (j < it.first[g] || j >= it.last[g]) return true;
+        // P beside S: S may be overwritten once the softmax has taken the tile
+        // before; P in S's place: the product that reads it was issued before
+        if (!C::kAliasP && sc[g] > 0 && !warp_wait(&s_free[g], (sc[g] - 1) & 1, w)) return false;
+        ++sc[g];
+        tc_fence_after();
+        const uint64_t qd = qdesc + (buf[g] * 2 + g) * kTile16, kd = kdesc + ks * kTile16;
+        if (lead) {
+#pragma unroll
+          for (int t = 0; t < 4 * NB; ++t)
+            if (t < ksteps)
+              tc_mma_f16_ss(tmem + C::kColS + 128 * g, qd + (t >> 2) * kBlock16 + (t & 3) * 2,
+                            kd + (t >> 2) * kBlock16 + (t & 3) * 2, idesc_s, t > 0 ? 1u : 0u);
+          tc_commit(&s_full[g]);
+          if (j == it.last[g] - 1) tc_commit(&q_empty[buf[g]][g]);
+        }
+        return true;
+      };
+      // O += P V of key tile j
+      const auto issue_pv = [&](int j, int g) {
+        if (j < it.first[g] || j >= it.last[g]) return true;
+        if (!warp_wait(&p_full[g], pc[g] & 1, w)) return false;
+        ++pc[g];
+        tc_fence_after();
+        const uint64_t vd = vdesc + vs * kTile16;
+        if (lead) {
+#pragma unroll
+          for (int t = 0; t < 8; ++t)  // 16 keys each
+            tc_mma_f16_ts(tmem + C::kColO + C::kStepO * g, tmem + C::kColP + C::kStepP * g + 8 * t, vd + t * 128,
+                          idesc_o, (j > it.first[g] || t > 0) ? 1u : 0u);
+          tc_commit(&pv_done[g]);
+        }
+        return true;
+      };
+      const auto k_release = [&] {
+        if (lead) tc_commit(&k_empty[ks]);
+        if (++ks == kStages) ks = 0, kph ^= 1;
+      };
+      const auto v_release = [&] {
+        if (lead) tc_commit(&v_empty[vs]);
+        if (++vs == kStages) vs = 0, vph ^= 1;
+      };
+      if constexpr (!C::kAliasP) {
+        if (warp == 9) {
+          for (int j = 0; ok && j < it.n; ++j) {
+            ok = warp_wait(&k_full[ks], kph, w) && issue_s(j, 0) && issue_s(j, 1);
+            if (ok) k_release();
+          }
+        } else {
+          for (int j = 0; ok && j < it.n; ++j) {
+            ok = warp_wait(&v_full[vs], vph, w) && issue_pv(j, 0) && issue_pv(j, 1);
+            if (ok) v_release();
+          }
+        }
+      } else {
+        ok = ok && warp_wait(&k_full[ks], kph, w) && issue_s(0, 0) && issue_s(0, 1);
+        if (ok) k_release();
+        for (int j = 0; ok && j < it.n; ++j) {
+          const bool more = j + 1 < it.n;
+          if (more) ok = warp_wait(&k_full[ks], kph, w);
+          ok = ok && warp_wait(&v_full[vs], vph, w);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            ok = ok && issue_pv(j, g);
+            if (more) ok = ok && issue_s(j + 1, g);
+          }
+          if (!ok) break;
+          v_release();
+          if (more) k_release();
+        }
+      }
     }
-    if (lane == 0) {
-      tc_commit(&drain_bar[g]);
-      mbar_wait_drain(&drain_bar[g], 0);
+    if (lead) {
+      tc_commit(&drain_bar[warp - 9]);
+      mbar_wait_drain(&drain_bar[warp - 9], 0);
     }
+    __syncwarp();
   }
   } else {
     regs_raise<kRegsSoftmax>();
@@ -535,6 +690,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t tS = tmem + C::kColS + 128 * g + lane_off, tO = tmem + C::kColO + C::kStepO * g + lane_off,
                    tP = tmem + C::kColP + C::kStepP * g + lane_off;
     const float c = a.scale * kLog2e;
+    CapPoly<BF> cap;
+    if constexpr ((MODE & kCap) != 0) cap.init(a.scale, a.cap);
     bool ok = true;
     uint32_t cnt = 0, kv = 0;  // this tile's key tiles so far, the CTA's
     for (int idx = blockIdx.x; ok && idx < p.n_items; idx += gridDim.x) {
@@ -548,96 +705,105 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const float slope2 = (MODE & kBias) && a.slopes ? __ldg(a.slopes + it.h) * kLog2e : 0.f;
       const int first = it.first[g], last = it.last[g];
       float m_run = -INFINITY, l_run = 0.f;
+      float s[128];  // the key tile's scores of this row
       for (int j = first; j < last; ++j, ++cnt) {
         const int base = it.lo + 128 * j;
-        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[g], cnt & 1, w))) {
+        const int rlo = rk.lo - base, rhi = rk.hi - base;
+        const bool cut = !__all_sync(0xffffffffu, rlo <= 0 && rhi >= 128);
+        if (!warp_wait(&s_full[g], cnt & 1, w)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        float s[128];
-        {
-          uint32_t u[64], v[64];
-          tmem_ld64(tS, u);
-          tmem_ld64(tS + 64, v);
-#pragma unroll
-          for (int e = 0; e < 64; ++e) {
-            s[e] = __uint_as_float(u[e]);
-            s[64 + e] = __uint_as_float(v[e]);
-          }
-        }
+        // the second half on its way while the first one's maximum is taken
+        tmem_ld32_nowait(tS, s);
+        tmem_ld32_nowait(tS + 32, s + 32);
+        tmem_wait_ld();
+        tmem_landed(s);
+        tmem_landed(s + 32);
+        tmem_ld32_nowait(tS + 64, s + 64);
+        tmem_ld32_nowait(tS + 96, s + 96);
+        const bool early = MODE == 0 && !cut;
+        float top = -INFINITY;
+        if (early) top = row_max<0, 64>(s, top);
+        tmem_wait_ld();
+        tmem_landed(s + 64);
+        tmem_landed(s + 96);
         if (!C::kAliasP) {
           tc_fence_before();
-          mbar_arrive(&s_free[g]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_free[g]);
         }
-        if constexpr (MODE != 0)
-          transform_scores<MODE, BF>(a, s, c, slope2, static_cast<float>(static_cast<long long>(rk.pos) - base));
-        const int rlo = rk.lo - base, rhi = rk.hi - base;
-        if (!__all_sync(0xffffffffu, rlo <= 0 && rhi >= 128)) {
+        bool raw = MODE == 0;  // exponents straight from the dot products
+        if constexpr ((MODE & kCap) != 0) {
+          const bool poly = __all_sync(0xffffffffu, cap.fits(row_max<0, 128, true>(s, 0.f)));
+          raw = MODE == kCap && poly && !cut;
+          if (!raw) finish_scores<MODE, BF>(s, cap, poly, c, slope2, static_cast<float>(static_cast<long long>(rk.pos) - base));
+        } else if constexpr (MODE == kBias) {
+          finish_scores<MODE, BF>(s, cap, false, c, slope2, static_cast<float>(static_cast<long long>(rk.pos) - base));
+        }
+        if (cut) {
 #pragma unroll
           for (int e = 0; e < 128; ++e) s[e] = (e >= rlo && e < rhi) ? s[e] : -INFINITY;
         }
-        float mx[4];
+        top = early ? row_max<64, 128>(s, top) : row_max<0, 128>(s, top);
+        if (MODE == 0) top *= c;
+        if constexpr (MODE == kCap) {
+          if (raw) {
+            if (a.scale < 0.f) {  // the smallest product gives the largest score
+              top = INFINITY;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) mx[t] = fmax3(s[t], s[4 + t], s[8 + t]);
-#pragma unroll
-        for (int e = 12; e < 124; e += 8) {
-#pragma unroll
-          for (int t = 0; t < 4; ++t) mx[t] = fmax3(mx[t], s[e + t], s[e + 4 + t]);
+              for (int e = 0; e < 128; ++e) top = fminf(top, s[e]);
+            }
+            const uint64_t t2 = f2_pack(top, top);
+            float unused;
+            f2_unpack(f2_mul(t2, cap.slope(t2)), top, unused);
+          }
         }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) mx[t] = fmaxf(mx[t], s[124 + t]);
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        const float m_new = fmaxf(m_run, MODE == 0 ? top * c : top);
+        const float m_new = fmaxf(m_run, top);
         const bool grow = m_new > m_run + kRescale;
-        const float alpha = grow ? ex2_approx(m_run - m_new) : 1.0f;  // exp2(-inf) = 0 on the first tile
-        l_run *= alpha;
-        if (grow) m_run = m_new;
+        const bool any_grow = __any_sync(0xffffffffu, grow);
+        float alpha = 1.0f;
+        if (any_grow && grow) {
+          alpha = ex2_approx(m_run - m_new);  // exp2(-inf) = 0 on the first tile
+          l_run *= alpha;
+          m_run = m_new;
+        }
         // a row that has seen no allowed key yet keeps m = -inf: all its p are 0
         const float m_use = m_run == -INFINITY ? 0.0f : m_run;
+        const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(-m_use, -m_use);
         if (j > first) {
           // O is stable (and, beside S, P free) once the product of the tile before is done
-          if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[g], (cnt - 1) & 1, w))) {
+          if (!warp_wait(&pv_done[g], (cnt - 1) & 1, w)) {
             ok = false;
             break;
           }
-          if (__any_sync(0xffffffffu, grow)) {
+          if (any_grow) {
             tc_fence_after();
 #pragma unroll 1
             for (int t = 0; t < a.d; t += 16) {
               uint32_t o[16];
               tmem_ld16(tO + t, o);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
               tmem_st16(tO + t, o);
             }
           }
         }
-        const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(-m_use, -m_use);
-        uint64_t sum2[2] = {0ull, 0ull};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const uint64_t v = f2_pack(s[32 * q + 2 * e], s[32 * q + 2 * e + 1]);
-            float xa, xb;
-            f2_unpack(MODE == 0 ? f2_fma(v, c2, nm2) : f2_add(v, nm2), xa, xb);
-            const float pa = ex2_approx(xa), pb = ex2_approx(xb);
-            sum2[e & 1] = f2_add(sum2[e & 1], f2_pack(pa, pb));
-            pk[e] = pack2<BF>(pa, pb);
-          }
-          tmem_st16_nowait(tP + 16 * q, pk);
+        if constexpr (MODE == kCap) {
+          if (raw)
+            l_run += exp_tile<FROM_CAP, 0, BF>(s, c2, nm2, cap, tP);
+          else
+            l_run += exp_tile<FROM_SCORE, 0, BF>(s, c2, nm2, cap, tP);
+        } else {
+          l_run += exp_tile<MODE == 0 ? FROM_DOT : FROM_SCORE, kPolyPairs<MODE>, BF>(s, c2, nm2, cap, tP);
         }
         tmem_wait_st();
-        float sa, sb;
-        f2_unpack(f2_add(sum2[0], sum2[1]), sa, sb);
-        l_run += sa + sb;
         if (j == it.n - 1 && it.hi - base < 128 && it.hi < a.Nk) {
           // values behind the last key that any row reads: zeros, since P's
           // zeros would not hide a NaN or an infinity there
           const uint32_t t = kv + static_cast<uint32_t>(j);
-          if (!__all_sync(0xffffffffu, mbar_wait(&v_full[t % kStages], (t / kStages) & 1, w))) {
+          if (!warp_wait(&v_full[t % kStages], (t / kStages) & 1, w)) {
             ok = false;
             break;
           }
@@ -648,12 +814,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           fence_proxy_async_smem();
         }
         tc_fence_before();
-        mbar_arrive(&p_full[g]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[g]);
       }
       kv += static_cast<uint32_t>(it.n);
       if (!ok) break;
       const bool some = last > first;
-      if (some && !__all_sync(0xffffffffu, mbar_wait(&pv_done[g], (cnt - 1) & 1, w))) {
+      if (some && !warp_wait(&pv_done[g], (cnt - 1) & 1, w)) {
         ok = false;
         break;
       }
@@ -695,6 +862,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       tc_fence_before();
     }
+    tmem_wait_ld();  // nothing in flight when the columns are given back
   }
   tc_fence_before();
   __syncthreads();
