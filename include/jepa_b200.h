@@ -463,8 +463,8 @@ typedef struct {
   const void *pos;          /* device: element (a, b, n) at pos[a * pos_stride_axis + b * pos_stride_b + n] */
   int64_t pos_stride_axis;
   int64_t pos_stride_b;     /* 0: every clip has the same positions */
-  const uint64_t *turns;    /* device [rot_dim / 2] */
-  const uint8_t *axis;      /* device [rot_dim / 2], each < n_axes (others count as axis 0); may be NULL for one axis */
+  const uint64_t *turns;    /* host [rot_dim / 2], read during the call */
+  const uint8_t *axis;      /* host [rot_dim / 2], each < n_axes, read during the call; may be NULL for one axis */
   float factor;             /* on cosine and sine (1 for a plain rotation) */
 } jepa_b200_rope;
 

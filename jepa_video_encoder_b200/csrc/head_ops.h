@@ -14,9 +14,9 @@ struct RopeParams {
   int rot_dim, half_layout, n_axes, pos_i64;
   const void* pos;
   long long pos_stride_axis, pos_stride_b;
-  const unsigned long long* turns;
-  const unsigned char* axis;
   float factor;
+  unsigned char axis[kMaxHeadDim / 2];
+  unsigned long long turns[kMaxHeadDim / 2];  // by value: a plan needs no device memory
 };
 
 // One tensor of a call: heads == 0 for a call that has only one.
@@ -28,6 +28,23 @@ struct HeadTensor {
   const float* weight;
   const float* bias;
   long long weight_h, bias_h;
+};
+
+// x / d for 0 <= x < 2^31 by a multiplication (Granlund and Montgomery's
+// division by an invariant): d <= 2^s, m = 2^32 (2^s - d) / d + 1.
+struct Div {
+  unsigned d, m, s;
+  void set(unsigned by) {
+    d = by;
+    s = 0;
+    while ((1ull << s) < by) ++s;
+    m = static_cast<unsigned>(((1ull << 32) * ((1ull << s) - by)) / by + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ unsigned operator()(unsigned x) const {
+    return static_cast<unsigned>((static_cast<unsigned long long>(__umulhi(x, m)) + x) >> s);
+  }
+#endif
 };
 
 struct HeadOpParams {

@@ -92,8 +92,7 @@ int fill_rope(RopeParams* r, const jepa_b200_rope& a, int d, int B) {
   if (a.layout != JEPA_B200_ROPE_HALF && a.layout != JEPA_B200_ROPE_INTERLEAVED) return JEPA_B200_ERR_ARG;
   if (a.rot_dim < 0 || a.rot_dim % 2 != 0 || a.rot_dim > d || a.n_axes < 1 || a.n_axes > 3) return JEPA_B200_ERR_SHAPE;
   if (!a.pos || !a.turns || (a.n_axes > 1 && !a.axis)) return JEPA_B200_ERR_ARG;
-  if ((a.pos_i64 != 0 && a.pos_i64 != 1) || (reinterpret_cast<uintptr_t>(a.pos) & (a.pos_i64 ? 7u : 3u)) != 0 ||
-      (reinterpret_cast<uintptr_t>(a.turns) & 7u) != 0)
+  if ((a.pos_i64 != 0 && a.pos_i64 != 1) || (reinterpret_cast<uintptr_t>(a.pos) & (a.pos_i64 ? 7u : 3u)) != 0)
     return JEPA_B200_ERR_ARG;
   if (a.pos_stride_axis < 0 || a.pos_stride_b < 0) return JEPA_B200_ERR_ARG;
   r->rot_dim = a.rot_dim;
@@ -103,9 +102,12 @@ int fill_rope(RopeParams* r, const jepa_b200_rope& a, int d, int B) {
   r->pos = a.pos;
   r->pos_stride_axis = a.n_axes > 1 ? a.pos_stride_axis : 0;
   r->pos_stride_b = B > 1 ? a.pos_stride_b : 0;
-  r->turns = reinterpret_cast<const unsigned long long*>(a.turns);
-  r->axis = a.n_axes > 1 ? a.axis : nullptr;
   r->factor = a.factor;
+  for (int i = 0; i < a.rot_dim / 2; ++i) {
+    r->turns[i] = a.turns[i];
+    r->axis[i] = a.n_axes > 1 ? a.axis[i] : 0;
+    if (r->axis[i] >= a.n_axes) return JEPA_B200_ERR_ARG;
+  }
   return JEPA_B200_OK;
 }
 

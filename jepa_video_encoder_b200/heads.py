@@ -13,8 +13,11 @@ refused while autograd records.
 from __future__ import annotations
 
 import math
-from dataclasses import dataclass
+from array import array
+from dataclasses import dataclass, field
 from typing import Any, Optional, Sequence, Tuple
+
+import torch
 
 from . import _abi
 from ._abi import check, load_library
@@ -25,52 +28,48 @@ _ATTN = _abi.packer(_abi.MaskedAttentionArgs)
 _LAYOUTS = {"half": _abi.ROPE_HALF, "interleaved": _abi.ROPE_INTERLEAVED}
 _NORMS = {"rms": _abi.NORM_RMS, "layer": _abi.NORM_LAYER}
 _NO_ROPE = (0, 0, 0, 0, 0, 0, 0, 0, 0, 0.0)
-_dtype_ids = {}
-
-
-def _ids():
-    if not _dtype_ids:
-        import torch
-        _dtype_ids.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: _abi.BF16})
-    return _dtype_ids
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: _abi.BF16}
 
 
 # ---------------------------------------------------------------- operands
 def _check_cuda(t, name: str, device: int) -> None:
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
-    if t.device.index != device:
+    if t.get_device() != device:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
         raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{device}")
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name} requires grad: the per-head operators are forward only (call them under "
                          "torch.no_grad() or on detached tensors)")
 
 
-def check_heads(t, name: str, dtype=None, shape: Optional[Sequence[int]] = None, granule: int = 1) -> None:
+def check_heads(t, name: str, dtype=None, shape: Optional[Sequence[int]] = None, granule: int = 1):
     """Validate the layout of a [B, N, heads, head_dim] operand: four axes,
     the last one contiguous; ``dtype`` and ``shape`` where they are set by
     another operand; with ``granule`` g > 1 a data pointer and strides that
-    are multiples of g elements."""
-    import torch
+    are multiples of g elements.  Returns (shape, (address, strides of the
+    first three axes))."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
-    if t.dim() != 4:
-        raise ValueError(f"{name} must be [B, N, heads, head_dim], got {list(t.shape)}")
+    have = t.shape
+    if len(have) != 4:
+        raise ValueError(f"{name} must be [B, N, heads, head_dim], got {list(have)}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.stride(3) != 1 and t.shape[3] > 1:
+    if shape is not None and have != shape and tuple(have) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(have)}")
+    sb, sn, sh, one = t.stride()
+    if one != 1 and have[3] > 1:
         raise ValueError(f"{name} must have a contiguous last axis")
-    if granule > 1 and t.numel():
-        if t.data_ptr() % (granule * t.element_size()):
+    at = t.data_ptr()
+    if granule > 1:
+        if at % (granule * t.element_size()):
             raise ValueError(f"{name} must start at a multiple of {granule * t.element_size()} bytes")
-        for n, s in zip(t.shape[:3], t.stride()[:3]):
-            if n > 1 and s % granule:
-                raise ValueError(f"{name}'s strides must be multiples of {granule} elements, got {t.stride()}")
+        if (sb | sn | sh) % granule:
+            for n, s in zip(have, (sb, sn, sh)):
+                if n > 1 and s % granule:
+                    raise ValueError(f"{name}'s strides must be multiples of {granule} elements, got {t.stride()}")
+            sb, sn, sh = (s if n > 1 else 0 for n, s in zip(have, (sb, sn, sh)))  # an axis of one has no stride
+    return have, (at, sb, sn, sh)
 
 
 def _span(t) -> int:
@@ -122,45 +121,41 @@ def _rows_apart(a, b) -> bool:
     return wide[0] <= off and off + wide[1] <= row
 
 
-def _strides(t) -> Tuple[int, int, int, int]:
-    s = t.stride()
-    return t.data_ptr(), s[0], s[1], s[2]
-
-
-def _launch(stream):
-    """(current device, raw stream) of a call."""
-    import torch
+def _launch(t, stream):
+    """(current device, raw stream) of a call on tensor t."""
+    if not t.is_cuda:
+        raise ValueError(f"expected CUDA tensors, got one on {t.device}")
     device = torch.cuda.current_device()
     if stream is None:
-        return device, torch.cuda.current_stream().cuda_stream
+        return device, torch.cuda.current_stream(device).cuda_stream
     if stream.device_index != device:
         raise ValueError(f"the stream is on cuda:{stream.device_index}, but the current device is cuda:{device}")
     return device, stream.cuda_stream
 
 
-def _new(like_shape, dtype, device: int, stream, zero: bool = False):
-    """An output of the call, owned by the stream that writes it."""
-    import torch
+def _new(like, device: int, stream, zero: bool = False):
+    """A contiguous output like an operand, owned by the stream that writes it."""
     make = torch.zeros if zero else torch.empty
     if stream is None:
-        return make(like_shape, dtype=dtype, device=device)
+        return make(like.shape, dtype=like.dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return make(like_shape, dtype=dtype, device=device)
+        return make(like.shape, dtype=like.dtype, device=like.device)
 
 
 # -------------------------------------------------------------- rotary plan
 @dataclass(frozen=True)
 class RopePlan:
-    """Frequencies of a rotation on one device (rope_plan makes it; a program
-    keeps it).  pairs of dims turn by position * inv_freq radians."""
+    """Frequencies of a rotation (rope_plan makes it; a program keeps it; it
+    serves every device).  Pairs of dims turn by position * inv_freq
+    radians."""
     rot_dim: int
     layout: str
     sections: Tuple[int, ...]
     inv_freq: Tuple[float, ...]   # radians per unit of position, one a pair
     factor: float                 # on cosine and sine
-    turns: Any                    # device int64 [pairs]: inv_freq / 2 pi as 64-bit binary fractions
-    axis: Any                     # device uint8 [pairs], None for one axis
-    device: int
+    turns: Any = field(repr=False)   # uint64 [pairs]: inv_freq / 2 pi as binary fractions
+    axis: Any = field(repr=False)    # uint8 [pairs]
+    addresses: Tuple[int, int] = field(repr=False)   # of turns and axis
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, sections: Optional[Sequence[int]] = None,
@@ -219,37 +214,34 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, sections: Optional[Seq
 
 
 def rope_turns(inv_freq: Sequence[float]):
-    """Radians per position as signed 64-bit words: the fraction of a turn per
+    """Radians per position as 64-bit words: the fraction of a turn per
     position times 2^64, rounded, modulo 2^64."""
-    words = [int(round(math.ldexp(math.fmod(w / (2 * math.pi), 1.0), 64))) % (1 << 64) for w in inv_freq]
-    return [w - (1 << 64) if w >= 1 << 63 else w for w in words]
+    return [int(round(math.ldexp(math.fmod(w / (2 * math.pi), 1.0), 64))) % (1 << 64) for w in inv_freq]
 
 
 def rope_plan(rot_dim: int, *, layout: str = "half", base: float = 10000.0, sections: Optional[Sequence[int]] = None,
-              scaling: Optional[dict] = None, device: Optional[int] = None) -> RopePlan:
+              scaling: Optional[dict] = None) -> RopePlan:
     """Plan of a rotation of the first rot_dim dims of every head.
 
     layout "half": pair i is dims (i, i + rot_dim / 2); "interleaved": dims
     (2i, 2i + 1).  sections: pairs of each position axis (the encoder's own
     3-D rotation is rope_plan(60, layout="interleaved", sections=(10, 10,
-    10))).  base, scaling: see rope_frequencies.  device: index of the CUDA
-    device (default: the current one)."""
-    import torch
+    10))).  base, scaling: see rope_frequencies."""
     if layout not in _LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
+    if rot_dim > 256:
+        raise ValueError(f"rot_dim must be at most 256, got {rot_dim}")
     freq, axis, factor = rope_frequencies(rot_dim, base, sections, scaling)
     sections = (rot_dim // 2,) if sections is None else tuple(int(n) for n in sections)
-    device = torch.cuda.current_device() if device is None else int(device)
-    turns = torch.tensor(rope_turns(freq), dtype=torch.int64, device=f"cuda:{device}")
-    axes = torch.tensor(axis, dtype=torch.uint8, device=f"cuda:{device}") if len(sections) > 1 else None
-    return RopePlan(rot_dim, layout, sections, freq, factor, turns, axes, device)
+    turns, axes = array("Q", rope_turns(freq)), array("B", axis)
+    return RopePlan(rot_dim, layout, sections, freq, factor, turns, axes,
+                    (turns.buffer_info()[0], axes.buffer_info()[0]))
 
 
 def check_positions(positions, n_axes: int, B: int, N: int) -> Tuple[int, int, int]:
     """Validate positions: int32 or int64, [N] or [B, N] for one axis, [axes,
     N] or [axes, B, N] for more, the token axis contiguous.  Returns (is
     int64, axis stride, batch stride)."""
-    import torch
     if not isinstance(positions, torch.Tensor):
         raise TypeError(f"positions must be a torch.Tensor, got {type(positions).__name__}")
     if positions.dtype not in (torch.int32, torch.int64):
@@ -276,17 +268,14 @@ def _rope_words(plan: RopePlan, positions, B: int, N: int, d: int, device: int):
     axes = len(plan.sections)
     i64, stride_axis, stride_b = check_positions(positions, axes, B, N)
     _check_cuda(positions, "positions", device)
-    if plan.device != device:
-        raise ValueError(f"the plan is on cuda:{plan.device}, but the current device is cuda:{device}")
     return (plan.rot_dim, _LAYOUTS[plan.layout], axes, i64, positions.data_ptr(), stride_axis, stride_b,
-            plan.turns.data_ptr(), 0 if plan.axis is None else plan.axis.data_ptr(), plan.factor)
+            *plan.addresses, plan.factor)
 
 
 def _float_type(t, name: str) -> int:
-    ids = _ids()
-    if t.dtype not in ids:
+    if t.dtype not in _DTYPES:
         raise ValueError(f"{name} must be float16, bfloat16 or float32, got {t.dtype}")
-    return ids[t.dtype]
+    return _DTYPES[t.dtype]
 
 
 def rope(x, positions, plan: RopePlan, out=None, stream=None):
@@ -296,29 +285,28 @@ def rope(x, positions, plan: RopePlan, out=None, stream=None):
     positions: integer tensor [N] (every clip the same) or [B, N], with
     several axes [axes, N] or [axes, B, N].  out: the tensor to write; x
     itself turns x in place."""
-    check_heads(x, "x")
-    B, N, H, d = x.shape
+    shape, at_x = check_heads(x, "x")
+    B, N, H, d = shape
     dtype = _float_type(x, "x")
-    device, raw = _launch(stream)
+    device, raw = _launch(x, stream)
     _check_cuda(x, "x", device)
     if not 1 <= d <= 256:
         raise ValueError(f"head_dim must be 1 to 256, got {d}")
     words = _rope_words(plan, positions, B, N, d, device)
     if out is None:
-        out = _new(x.shape, x.dtype, device, stream)
+        out = _new(x, device, stream)
+        at_out = check_heads(out, "out")[1]
     else:
-        check_heads(out, "out", x.dtype, x.shape)
+        at_out = check_heads(out, "out", x.dtype, shape)[1]
         _check_cuda(out, "out", device)
         check_output(out, "out", [(x, "x", True), (positions, "positions", False)])
-    if not x.numel():
+    if not (B and N and H):
         return out
-    check(load_library().jepa_b200_op_rope(_ROPE.pack(*_strides(x), *_strides(out), dtype, B, N, H, d, *words), raw),
-          "rope")
+    check(load_library().jepa_b200_op_rope(_ROPE.pack(*at_x, *at_out, dtype, B, N, H, d, *words), raw), "rope")
     return out
 
 
 def _weight(t, name: str, heads: int, d: int, device: int) -> Tuple[int, int]:
-    import torch
     if t is None:
         return 0, 0
     if not isinstance(t, torch.Tensor):
@@ -341,12 +329,12 @@ def qk_norm_rope(q, k, positions, plan: Optional[RopePlan], q_weight, k_weight, 
     [d], or [heads, d] of their own.  plan None (positions then None too):
     no rotation.  q_out, k_out: the tensors to write; q and k themselves for
     an update in place, or rows of a cache."""
-    check_heads(q, "q")
+    shape, at_q = check_heads(q, "q")
     dtype = _float_type(q, "q")
-    check_heads(k, "k", q.dtype)
-    B, N, hq, d = q.shape
-    hk = k.shape[2]
-    if tuple(k.shape) != (B, N, hk, d):
+    k_shape, at_k = check_heads(k, "k", q.dtype)
+    B, N, hq, d = shape
+    hk = k_shape[2]
+    if tuple(k_shape) != (B, N, hk, d):
         raise ValueError(f"k must be [{B}, {N}, heads, {d}] like q, got {list(k.shape)}")
     if norm not in _NORMS:
         raise ValueError(f"norm must be one of {sorted(_NORMS)}, got {norm!r}")
@@ -354,7 +342,7 @@ def qk_norm_rope(q, k, positions, plan: Optional[RopePlan], q_weight, k_weight, 
         raise ValueError(f"eps must not be negative, got {eps}")
     if not 1 <= d <= 256:
         raise ValueError(f"head_dim must be 1 to 256, got {d}")
-    device, raw = _launch(stream)
+    device, raw = _launch(q, stream)
     _check_cuda(q, "q", device)
     _check_cuda(k, "k", device)
     if q_weight is None or k_weight is None:
@@ -369,31 +357,34 @@ def qk_norm_rope(q, k, positions, plan: Optional[RopePlan], q_weight, k_weight, 
         words = _NO_ROPE
     else:
         words = _rope_words(plan, positions, B, N, d, device)
-    others = [(positions, "positions", False), (q_weight, "q_weight", False), (k_weight, "k_weight", False),
-              (q_bias, "q_bias", False), (k_bias, "k_bias", False)]
+    def others():
+        return [(positions, "positions", False), (q_weight, "q_weight", False), (k_weight, "k_weight", False),
+                (q_bias, "q_bias", False), (k_bias, "k_bias", False)]
+
     if q_out is None:
-        q_out = _new(q.shape, q.dtype, device, stream)
+        q_out = _new(q, device, stream)
+        at_qo = check_heads(q_out, "q_out")[1]
     else:
-        check_heads(q_out, "q_out", q.dtype, q.shape)
+        at_qo = check_heads(q_out, "q_out", q.dtype, shape)[1]
         _check_cuda(q_out, "q_out", device)
-        check_output(q_out, "q_out", [(q, "q", True), (k, "k", False)] + others)
+        check_output(q_out, "q_out", [(q, "q", True), (k, "k", False)] + others())
     if k_out is None:
-        k_out = _new(k.shape, k.dtype, device, stream)
+        k_out = _new(k, device, stream)
+        at_ko = check_heads(k_out, "k_out")[1]
     else:
-        check_heads(k_out, "k_out", q.dtype, k.shape)
+        at_ko = check_heads(k_out, "k_out", q.dtype, k_shape)[1]
         _check_cuda(k_out, "k_out", device)
-        check_output(k_out, "k_out", [(k, "k", True), (q, "q", False), (q_out, "q_out", False)] + others)
-    if not q.numel() and not k.numel():
+        check_output(k_out, "k_out", [(k, "k", True), (q, "q", False), (q_out, "q_out", False)] + others())
+    if not (B and N and (hq or hk)):
         return q_out, k_out
     check(load_library().jepa_b200_op_qk_norm_rope(
-        _QK.pack(*_strides(q), *_strides(k), *_strides(q_out), *_strides(k_out), dtype, B, N, hq, hk, d, _NORMS[norm],
-                 eps, qw, qb, kw, kb, qw_h, qb_h, kw_h, kb_h, *words), raw), "qk_norm_rope")
+        _QK.pack(*at_q, *at_k, *at_qo, *at_ko, dtype, B, N, hq, hk, d, _NORMS[norm], eps, qw, qb, kw, kb, qw_h, qb_h,
+                 kw_h, kb_h, *words), raw), "qk_norm_rope")
     return q_out, k_out
 
 
 def _per_clip(t, name: str, shape, device: int) -> int:
     """Device address of an int32 tensor that a kernel indexes per clip."""
-    import torch
     if t is None:
         return 0
     if not isinstance(t, torch.Tensor):
@@ -425,17 +416,16 @@ def masked_attention(q, k, v, *, scale: Optional[float] = None, cap: Optional[fl
     Rows that may read no key are zeros.  Rows outside every document are
     left as they are in ``out``, and are zeros where out is not given.  Keys
     and values that a row may not read do not reach it, whatever they hold."""
-    import torch
-    check_heads(q, "q", granule=8)
-    if q.dtype not in (torch.float16, torch.bfloat16):
+    shape, at_q = check_heads(q, "q", granule=8)
+    dtype = _DTYPES.get(q.dtype, 0)
+    if not dtype:
         raise ValueError(f"q must be float16 or bfloat16, got {q.dtype}")
-    dtype = _ids()[q.dtype]
-    check_heads(k, "k", q.dtype, granule=8)
-    check_heads(v, "v", q.dtype, k.shape, granule=8)
-    B, Nq, hq, d = q.shape
-    _, Nk, hk, _ = k.shape
-    if k.shape[0] != B or k.shape[3] != d:
-        raise ValueError(f"k must be [{B}, Nk, heads, {d}] like q, got {list(k.shape)}")
+    k_shape, at_k = check_heads(k, "k", q.dtype, granule=8)
+    _, at_v = check_heads(v, "v", q.dtype, k_shape, granule=8)
+    B, Nq, hq, d = shape
+    Bk, Nk, hk, dk = k_shape
+    if Bk != B or dk != d:
+        raise ValueError(f"k must be [{B}, Nk, heads, {d}] like q, got {list(k_shape)}")
     if hq < 1 or hk < 1 or hq % hk:
         raise ValueError(f"q's heads must be a multiple of k's, got {hq} and {hk}")
     if not 8 <= d <= 128 or d % 8:
@@ -448,7 +438,7 @@ def masked_attention(q, k, v, *, scale: Optional[float] = None, cap: Optional[fl
         raise ValueError(f"cap must be finite and not negative, got {cap}")
     if prefix is not None and not causal:
         raise ValueError("prefix needs causal")
-    device, raw = _launch(stream)
+    device, raw = _launch(q, stream)
     _check_cuda(q, "q", device)
     _check_cuda(k, "k", device)
     _check_cuda(v, "v", device)
@@ -471,17 +461,18 @@ def masked_attention(q, k, v, *, scale: Optional[float] = None, cap: Optional[fl
         if slopes.dim() != 1:
             raise ValueError(f"slopes must be [{hq}], got {list(slopes.shape)}")
     if out is None:
-        out = _new(q.shape, q.dtype, device, stream, zero=n_docs > 0)
+        out = _new(q, device, stream, zero=n_docs > 0)
+        at_out = check_heads(out, "out")[1]
     else:
-        check_heads(out, "out", q.dtype, q.shape, granule=8)
+        at_out = check_heads(out, "out", q.dtype, shape, granule=8)[1]
         _check_cuda(out, "out", device)
         check_output(out, "out", [(q, "q", False), (k, "k", False), (v, "v", False), (prefix, "prefix", False),
                                   (doc_offsets, "doc_offsets", False), (kv_len, "kv_len", False),
                                   (q_start, "q_start", False), (slopes, "slopes", False)])
-    if not q.numel():
+    if not (B and Nq):
         return out
     check(load_library().jepa_b200_op_masked_attention(
-        _ATTN.pack(*_strides(q), *_strides(k), *_strides(v), *_strides(out), dtype, B, Nq, Nk, hq, hk, d, scale, cap,
+        _ATTN.pack(*at_q, *at_k, *at_v, *at_out, dtype, B, Nq, Nk, hq, hk, d, scale, cap,
                    1 if causal else 0, n_docs, at_slopes, at_prefix, at_docs, at_len, at_start), raw),
         "masked_attention")
     return out

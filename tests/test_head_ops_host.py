@@ -240,7 +240,7 @@ ROPE_BAD = [(dict(dtype=2), _abi.ERR_DTYPE), (dict(head_dim=0), _abi.ERR_SHAPE),
             (dict(B=-1), _abi.ERR_SHAPE), (dict(B=65536, N=65536), _abi.ERR_SHAPE), (dict(rot_dim=66), _abi.ERR_SHAPE),
             (dict(rot_dim=3), _abi.ERR_SHAPE), (dict(rot_dim=-2), _abi.ERR_SHAPE), (dict(n_axes=4), _abi.ERR_SHAPE),
             (dict(n_axes=0), _abi.ERR_SHAPE), (dict(n_axes=3), _abi.ERR_ARG), (dict(layout=2), _abi.ERR_ARG),
-            (dict(pos=0), _abi.ERR_ARG), (dict(turns=0), _abi.ERR_ARG), (dict(turns=AT + 4), _abi.ERR_ARG),
+            (dict(pos=0), _abi.ERR_ARG), (dict(turns=0), _abi.ERR_ARG),
             (dict(pos=AT + 4), _abi.ERR_ARG), (dict(pos_i64=2), _abi.ERR_ARG), (dict(pos_stride_b=-1, B=2), _abi.ERR_ARG),
             (dict(x=_h(0)), _abi.ERR_ARG), (dict(x=_h(AT + 1)), _abi.ERR_ARG), (dict(out=_h(sn=8)), _abi.ERR_ARG)]
 
