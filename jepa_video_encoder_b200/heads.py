@@ -28,6 +28,10 @@ _ATTN = _abi.packer(_abi.MaskedAttentionArgs)
 _LAYOUTS = {"half": _abi.ROPE_HALF, "interleaved": _abi.ROPE_INTERLEAVED}
 _NORMS = {"rms": _abi.NORM_RMS, "layer": _abi.NORM_LAYER}
 _NO_ROPE = (0, 0, 0, 0, 0, 0, 0, 0, 0, 0.0)
+# the current stream's address without a Stream object, which costs more than
+# the rest of a call's checks together
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: _abi.BF16}
 
 
@@ -127,19 +131,23 @@ def _launch(t, stream):
         raise ValueError(f"expected CUDA tensors, got one on {t.device}")
     device = torch.cuda.current_device()
     if stream is None:
-        return device, torch.cuda.current_stream(device).cuda_stream
+        return device, _raw_stream(device)
     if stream.device_index != device:
         raise ValueError(f"the stream is on cuda:{stream.device_index}, but the current device is cuda:{device}")
     return device, stream.cuda_stream
 
 
-def _new(like, device: int, stream, zero: bool = False):
-    """A contiguous output like an operand, owned by the stream that writes it."""
-    make = torch.zeros if zero else torch.empty
+def _new(like, shape, stream, zero: bool = False):
+    """A contiguous output like an operand [B, N, h, d], owned by the stream
+    that writes it, and its (address, strides)."""
+    make = torch.zeros_like if zero else torch.empty_like
     if stream is None:
-        return make(like.shape, dtype=like.dtype, device=like.device)
-    with torch.cuda.stream(stream):
-        return make(like.shape, dtype=like.dtype, device=like.device)
+        out = make(like, memory_format=torch.contiguous_format)
+    else:
+        with torch.cuda.stream(stream):
+            out = make(like, memory_format=torch.contiguous_format)
+    _, N, h, d = shape
+    return out, (out.data_ptr(), N * h * d, h * d, d)
 
 
 # -------------------------------------------------------------- rotary plan
@@ -294,8 +302,7 @@ def rope(x, positions, plan: RopePlan, out=None, stream=None):
         raise ValueError(f"head_dim must be 1 to 256, got {d}")
     words = _rope_words(plan, positions, B, N, d, device)
     if out is None:
-        out = _new(x, device, stream)
-        at_out = check_heads(out, "out")[1]
+        out, at_out = _new(x, shape, stream)
     else:
         at_out = check_heads(out, "out", x.dtype, shape)[1]
         _check_cuda(out, "out", device)
@@ -307,16 +314,20 @@ def rope(x, positions, plan: RopePlan, out=None, stream=None):
 
 
 def _weight(t, name: str, heads: int, d: int, device: int) -> Tuple[int, int]:
+    """(address, elements from one head's values to the next's) of a float32
+    vector [d] or table [heads, d]."""
     if t is None:
         return 0, 0
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
     if t.dtype != torch.float32:
         raise ValueError(f"{name} must be float32, got {t.dtype}")
-    if tuple(t.shape) not in ((d,), (heads, d)) or (d > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{name} must be [{d}] or [{heads}, {d}] with a contiguous last axis, got {list(t.shape)}")
-    _check_cuda(t, name, device)
-    return t.data_ptr(), t.stride(0) if t.dim() == 2 else 0
+    shape, strides = t.shape, t.stride()
+    if (shape != (d,) and shape != (heads, d)) or (d > 1 and strides[-1] != 1):
+        raise ValueError(f"{name} must be [{d}] or [{heads}, {d}] with a contiguous last axis, got {list(shape)}")
+    if t.get_device() != device or t.requires_grad:
+        _check_cuda(t, name, device)
+    return t.data_ptr(), strides[0] if len(shape) == 2 else 0
 
 
 def qk_norm_rope(q, k, positions, plan: Optional[RopePlan], q_weight, k_weight, *, q_bias=None, k_bias=None,
@@ -362,15 +373,13 @@ def qk_norm_rope(q, k, positions, plan: Optional[RopePlan], q_weight, k_weight, 
                 (q_bias, "q_bias", False), (k_bias, "k_bias", False)]
 
     if q_out is None:
-        q_out = _new(q, device, stream)
-        at_qo = check_heads(q_out, "q_out")[1]
+        q_out, at_qo = _new(q, shape, stream)
     else:
         at_qo = check_heads(q_out, "q_out", q.dtype, shape)[1]
         _check_cuda(q_out, "q_out", device)
         check_output(q_out, "q_out", [(q, "q", True), (k, "k", False)] + others())
     if k_out is None:
-        k_out = _new(k, device, stream)
-        at_ko = check_heads(k_out, "k_out")[1]
+        k_out, at_ko = _new(k, k_shape, stream)
     else:
         at_ko = check_heads(k_out, "k_out", q.dtype, k_shape)[1]
         _check_cuda(k_out, "k_out", device)
@@ -461,8 +470,7 @@ def masked_attention(q, k, v, *, scale: Optional[float] = None, cap: Optional[fl
         if slopes.dim() != 1:
             raise ValueError(f"slopes must be [{hq}], got {list(slopes.shape)}")
     if out is None:
-        out = _new(q, device, stream, zero=n_docs > 0)
-        at_out = check_heads(out, "out")[1]
+        out, at_out = _new(q, shape, stream, zero=n_docs > 0)
     else:
         at_out = check_heads(out, "out", q.dtype, shape, granule=8)[1]
         _check_cuda(out, "out", device)
