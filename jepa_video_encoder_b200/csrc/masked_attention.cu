@@ -918,6 +918,411 @@ int launch_tiles_mode(const TileParams& p, const CUtensorMap* tm, cudaStream_t s
 
 }  // namespace
 
+// -------------------------------------------------------------- few queries --
+// One to a few query rows of each clip against a long cache: bound by the
+// bytes of K and V.  The rows that share a key head (Nq query positions by
+// heads_q / heads_kv heads) are the 8-wide N of m16n8k16 products, with the
+// keys (S^T = K Q^T) and then the dims (O^T = V^T P^T) as M: K and V go from
+// global memory straight into the A fragments, 16 bytes a load.  For K that
+// works because a dot product may take its dims in any order: a lane's 8
+// consecutive dims serve as the pairs of two products, Q's alike.  For V a
+// lane loads the same 8 dims of two neighbouring keys and interleaves them
+// (one byte permutation a fragment word).  P^T comes from S^T's accumulators
+// by a transposing move of 8 x 8 blocks.
+// A cluster of CTAs shares a clip's key head and splits its keys; each warp
+// keeps its own running maximum and sums over tiles of 32 keys, K of the next
+// tile in flight while this one's softmax runs; the parts are joined through
+// shared memory, then through the cluster's, so that no workspace is needed
+// and the order of the sums is fixed.
+namespace {
+
+constexpr int kStepWarps = 4, kStepKeys = 32;
+
+struct StepParams {
+  MaskedAttnParams a;
+  int chunks;  // groups of 8 NR rows of a key head
+  int splits;  // CTAs of a cluster
+};
+
+template <bool BF>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 8 x 8 matrix of 16-bit values, a row a lane quad: transposed.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// What a part with maximum m and sum l counts for against the maximum `top`
+// of all parts: 0 where it has no key (or only scores of -inf), NaN where its
+// only scores are NaN.
+__device__ __forceinline__ float part_factor(float m, float l, float top) {
+  if (m == -INFINITY) return l == 0.f ? 0.f : NAN;
+  return ex2_approx(m - top);
+}
+
+__device__ __forceinline__ uint4 load_16(const uint16_t* p, bool on) {
+  return on ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
+}
+
+}  // namespace
+
+template <int NB, bool BF, int NR>
+__global__ void __launch_bounds__(kStepWarps * 32) masked_step_kernel(const __grid_constant__ StepParams p) {
+  constexpr int kRows = 8 * NR, kDims = 64 * NB;
+  __shared__ float part_o[kStepWarps][kRows][kDims];
+  __shared__ float part_m[kStepWarps][kRows], part_l[kStepWarps][kRows];
+  __shared__ float cta_m[kRows], cta_l[kRows];
+  __shared__ unsigned again;  // rank 0: rows whose result is not finite
+  const MaskedAttnParams& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quad = lane >> 2, c4 = lane & 3;
+  const int rank = blockIdx.x % p.splits;
+  int unit = blockIdx.x / p.splits;
+  const int chunk = unit % p.chunks;
+  unit /= p.chunks;
+  const int hk = unit % a.hk, b = unit / a.hk;
+  const int group = a.hq / a.hk, row0 = chunk * kRows;
+  if (threadIdx.x == 0) again = 0u;
+  pdl_wait();
+  pdl_trigger();
+
+  // row lane of the chunk: query position i, its keys; all warps alike
+  RowKeys rk;
+  rk.lo = rk.hi = rk.pos = 0;
+  rk.written = false;
+  const bool row_on = lane < kRows && row0 + lane < a.Nq * group;
+  if (row_on) rk = row_keys(a, b, (row0 + lane) / group);
+  const bool any = rk.hi > rk.lo;
+  const int lo = __reduce_min_sync(0xffffffffu, any ? rk.lo : 0x7fffffff);
+  const int hi = __reduce_max_sync(0xffffffffu, any ? rk.hi : 0);
+  const int total = hi > lo ? hi - lo : 0;
+  const int per = ((total + p.splits - 1) / p.splits + kStepKeys - 1) / kStepKeys * kStepKeys;
+  const int k0 = lo + rank * per, k1 = min(hi, k0 + per);
+  const int tiles = total > 0 && k1 > k0 ? (k1 - k0 + kStepKeys - 1) / kStepKeys : 0;
+
+  // this lane's rows of S^T and O^T: 2 c4 and 2 c4 + 1 of each group of 8
+  int rlo[NR][2], rhi[NR][2], rpos[NR][2];
+  float slope2[NR][2];
+#pragma unroll
+  for (int x = 0; x < NR; ++x)
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int src = 8 * x + 2 * c4 + y;
+      // a row that is not there reads everything: it must not make tiles look cut
+      rlo[x][y] = __shfl_sync(0xffffffffu, row_on ? rk.lo : 0, src);
+      rhi[x][y] = __shfl_sync(0xffffffffu, row_on ? rk.hi : 0x7fffffff, src);
+      rpos[x][y] = __shfl_sync(0xffffffffu, rk.pos, src);
+      slope2[x][y] = a.slopes ? __ldg(a.slopes + hk * group + (row0 + src) % group) * kLog2e : 0.f;
+    }
+  // Q: row quad of each group, dims 8 (4 s + c4) .. + 7
+  uint4 qf[NR][2 * NB];
+#pragma unroll
+  for (int x = 0; x < NR; ++x) {
+    const int r = row0 + 8 * x + quad;
+    const bool on = r < a.Nq * group;
+    const uint16_t* q = a.q + b * a.q_b + (on ? r / group : 0) * a.q_n + (hk * group + (on ? r % group : 0)) * a.q_h;
+#pragma unroll
+    for (int s = 0; s < 2 * NB; ++s) qf[x][s] = load_16(q + 8 * (4 * s + c4), on && 8 * (4 * s + c4) < a.d);
+  }
+
+  const uint16_t* kbase = a.k + b * a.k_b + hk * a.k_h + 8 * c4;
+  const uint16_t* vbase = a.v + b * a.v_b + hk * a.v_h + 8 * quad;
+  uint4 kf[2][2][2 * NB];  // [16 keys][key quad, quad + 8][32 dims]
+  uint4 vf[2][4][NB];      // [16 keys][key 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9][64 dims]
+  const auto load_k = [&](int key0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int key = key0 + 16 * h + 8 * y + quad;
+        const uint16_t* src = kbase + key * a.k_n;
+#pragma unroll
+        for (int s = 0; s < 2 * NB; ++s) kf[h][y][s] = load_16(src + 32 * s, key < k1 && 8 * (4 * s + c4) < a.d);
+      }
+  };
+  const auto load_v = [&](int key0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int key = key0 + 16 * h + 2 * c4 + (y & 1) + 8 * (y >> 1);
+        const uint16_t* src = vbase + key * a.v_n;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) vf[h][y][n] = load_16(src + 64 * n, key < k1 && 8 * (8 * n + quad) < a.d);
+      }
+  };
+
+  float m[NR][2], l[NR][2], o[NR][NB][4][4];
+#pragma unroll
+  for (int x = 0; x < NR; ++x) {
+    m[x][0] = m[x][1] = -INFINITY;
+    l[x][0] = l[x][1] = 0.f;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) o[x][n][t][0] = o[x][n][t][1] = o[x][n][t][2] = o[x][n][t][3] = 0.f;
+  }
+  const float c = a.scale * kLog2e;
+  const float zs2 = a.cap > 0.f ? 2.0f * kLog2e * a.scale / a.cap : 0.f, kl = a.cap * kLog2e;
+  if (warp < tiles) {
+    load_k(k0 + warp * kStepKeys);
+    load_v(k0 + warp * kStepKeys);
+  }
+  for (int t = warp; t < tiles; t += kStepWarps) {
+    const int key0 = k0 + t * kStepKeys;
+    const bool more = t + kStepWarps < tiles;
+    float s[NR][2][4];
+#pragma unroll
+    for (int x = 0; x < NR; ++x)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        s[x][h][0] = s[x][h][1] = s[x][h][2] = s[x][h][3] = 0.f;
+#pragma unroll
+        for (int d = 0; d < 2 * NB; ++d) {
+          const uint4 u = kf[h][0][d], w = kf[h][1][d], q = qf[x][d];
+          const uint32_t a0[4] = {u.x, w.x, u.y, w.y}, a1[4] = {u.z, w.z, u.w, w.w};
+          mma_16816<BF>(s[x][h], a0, q.x, q.y);
+          mma_16816<BF>(s[x][h], a1, q.z, q.w);
+        }
+      }
+    if (more) load_k(key0 + kStepWarps * kStepKeys);
+    bool grow = false;
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      const bool cut = !__all_sync(0xffffffffu, rlo[x][0] <= key0 && rhi[x][0] >= key0 + kStepKeys && rlo[x][1] <= key0 &&
+                                                    rhi[x][1] >= key0 + kStepKeys);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = key0 + 16 * h + 8 * (e >> 1) + quad, y = e & 1;
+          float v = s[x][h][e];
+          if (a.cap > 0.f)
+            v = fmaf(-2.0f * kl, rcp_approx(1.0f + ex2_approx(v * zs2)), kl);
+          else
+            v *= c;
+          if (a.slopes) v -= slope2[x][y] * fabsf(static_cast<float>(static_cast<long long>(rpos[x][y]) - key));
+          if (cut && (key < rlo[x][y] || key >= rhi[x][y])) v = -INFINITY;
+          s[x][h][e] = v;
+          grow |= v > m[x][y] + kRescale;
+        }
+    }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int x = 0; x < NR; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          float top = fmaxf(fmaxf(s[x][0][y], s[x][0][y + 2]), fmaxf(s[x][1][y], s[x][1][y + 2]));
+#pragma unroll
+          for (int sh = 4; sh < 32; sh <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
+          if (top > m[x][y] + kRescale) {
+            const float alpha = ex2_approx(m[x][y] - top);  // 0 while there was none
+            m[x][y] = top;
+            l[x][y] *= alpha;
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                o[x][n][u][y] *= alpha;
+                o[x][n][u][y + 2] *= alpha;
+              }
+          }
+        }
+    }
+    uint32_t pf[NR][2][2];
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      const float m0 = m[x][0] == -INFINITY ? 0.f : m[x][0], m1 = m[x][1] == -INFINITY ? 0.f : m[x][1];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float p0 = ex2_approx(s[x][h][0] - m0), p1 = ex2_approx(s[x][h][1] - m1);
+        const float p2 = ex2_approx(s[x][h][2] - m0), p3 = ex2_approx(s[x][h][3] - m1);
+        l[x][0] += p0 + p2;
+        l[x][1] += p1 + p3;
+        pf[x][h][0] = transpose_8x8(pack2<BF>(p0, p1));
+        pf[x][h][1] = transpose_8x8(pack2<BF>(p2, p3));
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const uint4 e0 = vf[h][0][n], e1 = vf[h][1][n], e2 = vf[h][2][n], e3 = vf[h][3][n];
+        const uint32_t w0[4] = {e0.x, e0.y, e0.z, e0.w}, w1[4] = {e1.x, e1.y, e1.z, e1.w};
+        const uint32_t w2[4] = {e2.x, e2.y, e2.z, e2.w}, w3[4] = {e3.x, e3.y, e3.z, e3.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t af[4] = {__byte_perm(w0[u], w1[u], 0x5410), __byte_perm(w0[u], w1[u], 0x7632),
+                                  __byte_perm(w2[u], w3[u], 0x5410), __byte_perm(w2[u], w3[u], 0x7632)};
+#pragma unroll
+          for (int x = 0; x < NR; ++x) mma_16816<BF>(o[x][n][u], af, pf[x][h][0], pf[x][h][1]);
+        }
+      }
+    if (more) load_v(key0 + kStepWarps * kStepKeys);
+  }
+
+  // the warp's part: lane holds dims 64 n + 8 quad + 2 u, + 1 of its rows
+#pragma unroll
+  for (int x = 0; x < NR; ++x)
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      float sum = l[x][y];
+#pragma unroll
+      for (int sh = 4; sh < 32; sh <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, sh);
+      const int r = 8 * x + 2 * c4 + y;
+      if (quad == 0) {
+        part_m[warp][r] = m[x][y];
+        part_l[warp][r] = sum;
+      }
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          *reinterpret_cast<float2*>(&part_o[warp][r][64 * n + 8 * quad + 2 * u]) = make_float2(o[x][n][u][y], o[x][n][u][y + 2]);
+    }
+  __syncthreads();
+  // the CTA's part, in place of warp 0's
+  if (threadIdx.x < kRows) {
+    const int r = threadIdx.x;
+    float mm = part_m[0][r];
+#pragma unroll
+    for (int v = 1; v < kStepWarps; ++v) mm = fmaxf(mm, part_m[v][r]);
+    float ll = 0.f;
+#pragma unroll
+    for (int v = 0; v < kStepWarps; ++v) {
+      const float f = part_factor(part_m[v][r], part_l[v][r], mm);
+      ll += part_l[v][r] * f;
+      part_m[v][r] = f;  // from here on the part's factor
+    }
+    cta_m[r] = mm;
+    cta_l[r] = ll;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kRows * kDims; i += kStepWarps * 32) {
+    const int r = i / kDims, d = i % kDims;
+    float v = 0.f;
+#pragma unroll
+    for (int x = 0; x < kStepWarps; ++x)
+      if (!(part_m[x][r] == 0.f)) v = fmaf(part_o[x][r][d], part_m[x][r], v);
+    part_o[0][r][d] = v;
+  }
+  if (p.splits > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  // Each CTA of the cluster joins and writes its share of the values.
+  const int share = (kRows * kDims / 8 + p.splits - 1) / p.splits;  // pieces of 8 dims
+  const uint32_t at_o = smem_u32(&part_o[0][0][0]), at_m = smem_u32(cta_m), at_l = smem_u32(cta_l);
+  const uint32_t at_again = p.splits > 1 ? mapa_shared(smem_u32(&again), 0) : smem_u32(&again);
+  for (int i = rank * share + threadIdx.x; i < min((rank + 1) * share, kRows * kDims / 8); i += kStepWarps * 32) {
+    const int r = i / (kDims / 8), d = i % (kDims / 8) * 8;
+    const int row = row0 + r;
+    if (row >= a.Nq * group || d >= a.d) continue;
+    const RowKeys k = row_keys(a, b, row / group);
+    if (!k.written) continue;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, ll = 0.f, mm = -INFINITY;
+    for (int x = 0; x < p.splits; ++x)
+      mm = fmaxf(mm, p.splits > 1 ? ld_cluster_f32(mapa_shared(at_m + 4 * r, x)) : cta_m[r]);
+    for (int x = 0; x < p.splits; ++x) {
+      const float mx = p.splits > 1 ? ld_cluster_f32(mapa_shared(at_m + 4 * r, x)) : cta_m[r];
+      const float lx = p.splits > 1 ? ld_cluster_f32(mapa_shared(at_l + 4 * r, x)) : cta_l[r];
+      const float f = part_factor(mx, lx, mm);
+      if (f == 0.f) continue;
+      ll = fmaf(lx, f, ll);
+      const uint32_t from = p.splits > 1 ? mapa_shared(at_o + 4 * (r * kDims + d), x) : 0u;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        v[e] = fmaf(p.splits > 1 ? ld_cluster_f32(from + 4 * e) : part_o[0][r][d + e], f, v[e]);
+    }
+    const bool some = k.hi > k.lo;
+    const float inv = some ? 1.0f / ll : 0.f;
+    float odd = 0.f;
+    uint32_t h[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = some ? v[2 * e] * inv : 0.f, y = some ? v[2 * e + 1] * inv : 0.f;
+      odd = fmaf(x, 0.f, fmaf(y, 0.f, odd));
+      h[e] = pack2<BF>(x, y);
+    }
+    *reinterpret_cast<uint4*>(a.out + b * a.o_b + (row / group) * a.o_n + (hk * group + row % group) * a.o_h + d) =
+        make_uint4(h[0], h[1], h[2], h[3]);
+    // as in the tiles: a value that is not finite may have come from a key
+    // that its row does not read
+    if (some && !(odd == 0.f))
+      asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(at_again), "r"(1u << r) : "memory");
+  }
+  if (p.splits > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  if (rank == 0 && again != 0u) {
+    for (int r = warp; r < kRows; r += kStepWarps) {
+      if (!((again >> r) & 1u)) continue;
+      const int row = row0 + r;
+      const RowKeys k = row_keys(a, b, row / group);
+      attend_row<BF>(a, b, row / group, hk * group + row % group, k, lane);
+    }
+  }
+}
+
+namespace {
+
+template <int NB, bool BF, int NR>
+int launch_step(const MaskedAttnParams& a, cudaStream_t st) {
+  StepParams p;
+  p.a = a;
+  const int rows = a.Nq * (a.hq / a.hk);
+  p.chunks = (rows + 8 * NR - 1) / (8 * NR);
+  const long long units = static_cast<long long>(a.B) * a.hk * p.chunks;
+  // Clusters as large as it takes to give every SM three CTAs, while a CTA
+  // keeps 256 keys, two tiles a warp.
+  p.splits = 1;
+  while (p.splits < 16 && units * p.splits < 3ll * num_sms() && a.Nk >= 2 * p.splits * 256) p.splits *= 2;
+  if (units * p.splits > 0x7fffffffll) return JEPA_B200_ERR_SHAPE;
+  auto kern = masked_step_kernel<NB, BF, NR>;
+  if (p.splits > 8) {  // beyond the portable size
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return JEPA_B200_ERR_CUDA;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if (!bit || !(done.load(std::memory_order_acquire) & bit)) {
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return JEPA_B200_ERR_CUDA;
+      done.fetch_or(bit, std::memory_order_release);
+    }
+  }
+  return launch_pdl(kern, dim3(static_cast<unsigned>(units * p.splits)), dim3(kStepWarps * 32), 0, st, p.splits, p) ==
+                 cudaSuccess
+             ? JEPA_B200_OK
+             : JEPA_B200_ERR_CUDA;
+}
+
+template <int NB, bool BF>
+int launch_step_rows(const MaskedAttnParams& a, cudaStream_t st) {
+  return a.Nq * (a.hq / a.hk) <= 8 ? launch_step<NB, BF, 1>(a, st) : launch_step<NB, BF, 2>(a, st);
+}
+
+}  // namespace
+
 int masked_attention_take_error(unsigned* code) {
   DevErr h{0, 0};
   if (cudaMemcpyFromSymbol(&h, g_masked_err, sizeof(h)) != cudaSuccess) return JEPA_B200_ERR_CUDA;
@@ -929,8 +1334,14 @@ int masked_attention_take_error(unsigned* code) {
   return JEPA_B200_OK;
 }
 
+// Query positions up to which the rows go to the few-query kernel.
+constexpr int kStepQueries = 16;
+
 int launch_masked_attention(const MaskedAttnParams& p, bool bf16, cudaStream_t st) {
-  if (p.Nq > 16) {
+  if (p.Nq <= kStepQueries) {
+    if (p.d <= 64) return bf16 ? launch_step_rows<1, true>(p, st) : launch_step_rows<1, false>(p, st);
+    return bf16 ? launch_step_rows<2, true>(p, st) : launch_step_rows<2, false>(p, st);
+  } else {
     TileParams tp;
     tp.a = p;
     tp.n_pairs = (p.Nq + 255) / 256;
