@@ -936,7 +936,11 @@ int launch_tiles_mode(const TileParams& p, const CUtensorMap* tm, cudaStream_t s
 // and the order of the sums is fixed.
 namespace {
 
-constexpr int kStepWarps = 4, kStepKeys = 32;
+constexpr int kStepKeys = 32;  // keys of a warp's tile (64 for heads of 64: 41 us in place of 34 at 32 x 12 heads, 2048 keys)
+
+// CTAs an SM holds, by the registers of K and V in flight.
+template <int NB, int NR, int WARPS>
+constexpr int kStepResident = WARPS == 8 ? 1 : (NB == 1 && NR == 1 ? 3 : 2);
 
 struct StepParams {
   MaskedAttnParams a;
@@ -985,13 +989,14 @@ __device__ __forceinline__ uint4 load_16(const uint16_t* p, bool on) {
 
 }  // namespace
 
-template <int NB, bool BF, int NR>
-__global__ void __launch_bounds__(kStepWarps * 32) masked_step_kernel(const __grid_constant__ StepParams p) {
-  constexpr int kRows = 8 * NR, kDims = 64 * NB;
-  __shared__ float part_o[kStepWarps][kRows][kDims];
-  __shared__ float part_m[kStepWarps][kRows], part_l[kStepWarps][kRows];
+template <int NB, bool BF, int NR, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, kStepResident<NB, NR, WARPS>) masked_step_kernel(const __grid_constant__ StepParams p) {
+  constexpr int kRows = 8 * NR, kDims = 64 * NB, kKeys = kStepKeys, kH = kKeys / 16;
+  __shared__ float part_o[WARPS][kRows][kDims];
+  __shared__ float part_m[WARPS][kRows], part_l[WARPS][kRows];
   __shared__ float cta_m[kRows], cta_l[kRows];
-  __shared__ unsigned again;  // rank 0: rows whose result is not finite
+  __shared__ unsigned again;    // rank 0: rows whose result is not finite
+  __shared__ int row_some[kRows];  // the row has keys (1), has none (0), is not written (-1)
   const MaskedAttnParams& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = lane >> 2, c4 = lane & 3;
@@ -1012,12 +1017,13 @@ __global__ void __launch_bounds__(kStepWarps * 32) masked_step_kernel(const __gr
   const bool row_on = lane < kRows && row0 + lane < a.Nq * group;
   if (row_on) rk = row_keys(a, b, (row0 + lane) / group);
   const bool any = rk.hi > rk.lo;
+  if (warp == 0 && lane < kRows) row_some[lane] = rk.written ? (any ? 1 : 0) : -1;
   const int lo = __reduce_min_sync(0xffffffffu, any ? rk.lo : 0x7fffffff);
   const int hi = __reduce_max_sync(0xffffffffu, any ? rk.hi : 0);
   const int total = hi > lo ? hi - lo : 0;
-  const int per = ((total + p.splits - 1) / p.splits + kStepKeys - 1) / kStepKeys * kStepKeys;
+  const int per = ((total + p.splits - 1) / p.splits + kKeys - 1) / kKeys * kKeys;
   const int k0 = lo + rank * per, k1 = min(hi, k0 + per);
-  const int tiles = total > 0 && k1 > k0 ? (k1 - k0 + kStepKeys - 1) / kStepKeys : 0;
+  const int tiles = total > 0 && k1 > k0 ? (k1 - k0 + kKeys - 1) / kKeys : 0;
 
   // this lane's rows of S^T and O^T: 2 c4 and 2 c4 + 1 of each group of 8
   int rlo[NR][2], rhi[NR][2], rpos[NR][2];
@@ -1044,30 +1050,36 @@ __global__ void __launch_bounds__(kStepWarps * 32) masked_step_kernel(const __gr
     for (int s = 0; s < 2 * NB; ++s) qf[x][s] = load_16(q + 8 * (4 * s + c4), on && 8 * (4 * s + c4) < a.d);
   }
 
-  const uint16_t* kbase = a.k + b * a.k_b + hk * a.k_h + 8 * c4;
-  const uint16_t* vbase = a.v + b * a.v_b + hk * a.v_h + 8 * quad;
-  uint4 kf[2][2][2 * NB];  // [16 keys][key quad, quad + 8][32 dims]
-  uint4 vf[2][4][NB];      // [16 keys][key 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9][64 dims]
+  // Loads need no bounds but the clamps here: a key behind the last one is
+  // read as the last (its score is masked), dims behind d as the first ones
+  // (Q has zeros there, and O's are not stored).
+  int koff[2 * NB], voff[NB];
+#pragma unroll
+  for (int s = 0; s < 2 * NB; ++s) koff[s] = 8 * (4 * s + c4) < a.d ? 8 * (4 * s + c4) : 0;
+#pragma unroll
+  for (int n = 0; n < NB; ++n) voff[n] = 8 * (8 * n + quad) < a.d ? 8 * (8 * n + quad) : 0;
+  const uint16_t* kbase = a.k + b * a.k_b + hk * a.k_h;
+  const uint16_t* vbase = a.v + b * a.v_b + hk * a.v_h;
+  uint4 kf[kH][2][2 * NB];  // [16 keys][key quad, quad + 8][32 dims]
+  uint4 vf[kH][4][NB];      // [16 keys][key 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9][64 dims]
   const auto load_k = [&](int key0) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < kH; ++h)
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const int key = key0 + 16 * h + 8 * y + quad;
-        const uint16_t* src = kbase + key * a.k_n;
+        const uint16_t* src = kbase + min(key0 + 16 * h + 8 * y + quad, k1 - 1) * a.k_n;
 #pragma unroll
-        for (int s = 0; s < 2 * NB; ++s) kf[h][y][s] = load_16(src + 32 * s, key < k1 && 8 * (4 * s + c4) < a.d);
+        for (int s = 0; s < 2 * NB; ++s) kf[h][y][s] = __ldg(reinterpret_cast<const uint4*>(src + koff[s]));
       }
   };
   const auto load_v = [&](int key0) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < kH; ++h)
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        const int key = key0 + 16 * h + 2 * c4 + (y & 1) + 8 * (y >> 1);
-        const uint16_t* src = vbase + key * a.v_n;
+        const uint16_t* src = vbase + min(key0 + 16 * h + 2 * c4 + (y & 1) + 8 * (y >> 1), k1 - 1) * a.v_n;
 #pragma unroll
-        for (int n = 0; n < NB; ++n) vf[h][y][n] = load_16(src + 64 * n, key < k1 && 8 * (8 * n + quad) < a.d);
+        for (int n = 0; n < NB; ++n) vf[h][y][n] = __ldg(reinterpret_cast<const uint4*>(src + voff[n]));
       }
   };
 
@@ -1084,17 +1096,17 @@ __global__ void __launch_bounds__(kStepWarps * 32) masked_step_kernel(const __gr
   const float c = a.scale * kLog2e;
   const float zs2 = a.cap > 0.f ? 2.0f * kLog2e * a.scale / a.cap : 0.f, kl = a.cap * kLog2e;
   if (warp < tiles) {
-    load_k(k0 + warp * kStepKeys);
-    load_v(k0 + warp * kStepKeys);
+    load_k(k0 + warp * kKeys);
+    load_v(k0 + warp * kKeys);
   }
-  for (int t = warp; t < tiles; t += kStepWarps) {
-    const int key0 = k0 + t * kStepKeys;
-    const bool more = t + kStepWarps < tiles;
-    float s[NR][2][4];
+  for (int t = warp; t < tiles; t += WARPS) {
+    const int key0 = k0 + t * kKeys;
+    const bool more = t + WARPS < tiles;
+    float s[NR][kH][4];
 #pragma unroll
     for (int x = 0; x < NR; ++x)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kH; ++h) {
         s[x][h][0] = s[x][h][1] = s[x][h][2] = s[x][h][3] = 0.f;
 #pragma unroll
         for (int d = 0; d < 2 * NB; ++d) {
@@ -1104,39 +1116,64 @@ __global__ void __launch_bounds__(kStepWarps * 32) masked_step_kernel(const __gr
           mma_16816<BF>(s[x][h], a1, q.z, q.w);
         }
       }
-    if (more) load_k(key0 + kStepWarps * kStepKeys);
-    bool grow = false;
+    if (more) load_k(key0 + WARPS * kKeys);
+    if (a.cap > 0.f) {
 #pragma unroll
-    for (int x = 0; x < NR; ++x) {
-      const bool cut = !__all_sync(0xffffffffu, rlo[x][0] <= key0 && rhi[x][0] >= key0 + kStepKeys && rlo[x][1] <= key0 &&
-                                                    rhi[x][1] >= key0 + kStepKeys);
+      for (int i = 0; i < 4 * kH * NR; ++i) {
+        float& v = s[i / (4 * kH)][(i >> 2) % kH][i & 3];
+        v = fmaf(-2.0f * kl, rcp_approx(1.0f + ex2_approx(v * zs2)), kl);
+      }
+    } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int i = 0; i < 4 * kH * NR; ++i) s[i / (4 * kH)][(i >> 2) % kH][i & 3] *= c;
+    }
+    if (a.slopes) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = key0 + 16 * h + 8 * (e >> 1) + quad, y = e & 1;
-          float v = s[x][h][e];
-          if (a.cap > 0.f)
-            v = fmaf(-2.0f * kl, rcp_approx(1.0f + ex2_approx(v * zs2)), kl);
-          else
-            v *= c;
-          if (a.slopes) v -= slope2[x][y] * fabsf(static_cast<float>(static_cast<long long>(rpos[x][y]) - key));
-          if (cut && (key < rlo[x][y] || key >= rhi[x][y])) v = -INFINITY;
-          s[x][h][e] = v;
-          grow |= v > m[x][y] + kRescale;
+      for (int x = 0; x < NR; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const float far = static_cast<float>(static_cast<long long>(rpos[x][y]) - key0 - quad);
+#pragma unroll
+          for (int h = 0; h < kH; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) s[x][h][2 * e + y] -= slope2[x][y] * fabsf(far - static_cast<float>(16 * h + 8 * e));
         }
     }
+    bool whole = true;  // no row's interval cuts the tile
+#pragma unroll
+    for (int x = 0; x < NR; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) whole = whole && rlo[x][y] <= key0 && rhi[x][y] >= key0 + kKeys;
+    if (!__all_sync(0xffffffffu, whole)) {
+#pragma unroll
+      for (int i = 0; i < 4 * kH * NR; ++i) {
+        const int x = i / (4 * kH), h = (i >> 2) % kH, e = i & 3, key = key0 + 16 * h + 8 * (e >> 1) + quad;
+        if (key < rlo[x][e & 1] || key >= rhi[x][e & 1]) s[x][h][e] = -INFINITY;
+      }
+    }
+    bool grow = false;
+    float top[NR][2];
+#pragma unroll
+    for (int x = 0; x < NR; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+        {
+          top[x][y] = fmaxf(s[x][0][y], s[x][0][y + 2]);
+#pragma unroll
+          for (int h = 1; h < kH; ++h) top[x][y] = fmax3(top[x][y], s[x][h][y], s[x][h][y + 2]);
+          grow |= top[x][y] > m[x][y] + kRescale;
+        }
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
       for (int x = 0; x < NR; ++x)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          float top = fmaxf(fmaxf(s[x][0][y], s[x][0][y + 2]), fmaxf(s[x][1][y], s[x][1][y + 2]));
+          float mx = top[x][y];
 #pragma unroll
-          for (int sh = 4; sh < 32; sh <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
-          if (top > m[x][y] + kRescale) {
-            const float alpha = ex2_approx(m[x][y] - top);  // 0 while there was none
-            m[x][y] = top;
+          for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+          if (mx > m[x][y] + kRescale) {
+            const float alpha = ex2_approx(m[x][y] - mx);  // 0 while there was none
+            m[x][y] = mx;
             l[x][y] *= alpha;
 #pragma unroll
             for (int n = 0; n < NB; ++n)
@@ -1148,12 +1185,12 @@ __global__ void __launch_bounds__(kStepWarps * 32) masked_step_kernel(const __gr
           }
         }
     }
-    uint32_t pf[NR][2][2];
+    uint32_t pf[NR][kH][2];
 #pragma unroll
     for (int x = 0; x < NR; ++x) {
       const float m0 = m[x][0] == -INFINITY ? 0.f : m[x][0], m1 = m[x][1] == -INFINITY ? 0.f : m[x][1];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kH; ++h) {
         const float p0 = ex2_approx(s[x][h][0] - m0), p1 = ex2_approx(s[x][h][1] - m1);
         const float p2 = ex2_approx(s[x][h][2] - m0), p3 = ex2_approx(s[x][h][3] - m1);
         l[x][0] += p0 + p2;
@@ -1163,7 +1200,7 @@ __global__ void __launch_bounds__(kStepWarps * 32) masked_step_kernel(const __gr
       }
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < kH; ++h)
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
         const uint4 e0 = vf[h][0][n], e1 = vf[h][1][n], e2 = vf[h][2][n], e3 = vf[h][3][n];
@@ -1177,7 +1214,7 @@ __global__ void __launch_bounds__(kStepWarps * 32) masked_step_kernel(const __gr
           for (int x = 0; x < NR; ++x) mma_16816<BF>(o[x][n][u], af, pf[x][h][0], pf[x][h][1]);
         }
       }
-    if (more) load_v(key0 + kStepWarps * kStepKeys);
+    if (more) load_v(key0 + WARPS * kKeys);
   }
 
   // the warp's part: lane holds dims 64 n + 8 quad + 2 u, + 1 of its rows
@@ -1205,10 +1242,10 @@ __global__ void __launch_bounds__(kStepWarps * 32) masked_step_kernel(const __gr
     const int r = threadIdx.x;
     float mm = part_m[0][r];
 #pragma unroll
-    for (int v = 1; v < kStepWarps; ++v) mm = fmaxf(mm, part_m[v][r]);
+    for (int v = 1; v < WARPS; ++v) mm = fmaxf(mm, part_m[v][r]);
     float ll = 0.f;
 #pragma unroll
-    for (int v = 0; v < kStepWarps; ++v) {
+    for (int v = 0; v < WARPS; ++v) {
       const float f = part_factor(part_m[v][r], part_l[v][r], mm);
       ll += part_l[v][r] * f;
       part_m[v][r] = f;  // from here on the part's factor
@@ -1217,11 +1254,11 @@ __global__ void __launch_bounds__(kStepWarps * 32) masked_step_kernel(const __gr
     cta_l[r] = ll;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < kRows * kDims; i += kStepWarps * 32) {
+  for (int i = threadIdx.x; i < kRows * kDims; i += WARPS * 32) {
     const int r = i / kDims, d = i % kDims;
     float v = 0.f;
 #pragma unroll
-    for (int x = 0; x < kStepWarps; ++x)
+    for (int x = 0; x < WARPS; ++x)
       if (!(part_m[x][r] == 0.f)) v = fmaf(part_o[x][r][d], part_m[x][r], v);
     part_o[0][r][d] = v;
   }
@@ -1233,12 +1270,10 @@ __global__ void __launch_bounds__(kStepWarps * 32) masked_step_kernel(const __gr
   const int share = (kRows * kDims / 8 + p.splits - 1) / p.splits;  // pieces of 8 dims
   const uint32_t at_o = smem_u32(&part_o[0][0][0]), at_m = smem_u32(cta_m), at_l = smem_u32(cta_l);
   const uint32_t at_again = p.splits > 1 ? mapa_shared(smem_u32(&again), 0) : smem_u32(&again);
-  for (int i = rank * share + threadIdx.x; i < min((rank + 1) * share, kRows * kDims / 8); i += kStepWarps * 32) {
+  for (int i = rank * share + threadIdx.x; i < min((rank + 1) * share, kRows * kDims / 8); i += WARPS * 32) {
     const int r = i / (kDims / 8), d = i % (kDims / 8) * 8;
     const int row = row0 + r;
-    if (row >= a.Nq * group || d >= a.d) continue;
-    const RowKeys k = row_keys(a, b, row / group);
-    if (!k.written) continue;
+    if (row_some[r] < 0 || d >= a.d) continue;  // (a row behind the last one neither)
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, ll = 0.f, mm = -INFINITY;
     for (int x = 0; x < p.splits; ++x)
       mm = fmaxf(mm, p.splits > 1 ? ld_cluster_f32(mapa_shared(at_m + 4 * r, x)) : cta_m[r]);
@@ -1253,7 +1288,7 @@ __global__ void __launch_bounds__(kStepWarps * 32) masked_step_kernel(const __gr
       for (int e = 0; e < 8; ++e)
         v[e] = fmaf(p.splits > 1 ? ld_cluster_f32(from + 4 * e) : part_o[0][r][d + e], f, v[e]);
     }
-    const bool some = k.hi > k.lo;
+    const bool some = row_some[r] > 0;
     const float inv = some ? 1.0f / ll : 0.f;
     float odd = 0.f;
     uint32_t h[4];
@@ -1275,7 +1310,7 @@ __global__ void __launch_bounds__(kStepWarps * 32) masked_step_kernel(const __gr
   else
     __syncthreads();
   if (rank == 0 && again != 0u) {
-    for (int r = warp; r < kRows; r += kStepWarps) {
+    for (int r = warp; r < kRows; r += WARPS) {
       if (!((again >> r) & 1u)) continue;
       const int row = row0 + r;
       const RowKeys k = row_keys(a, b, row / group);
@@ -1286,6 +1321,44 @@ __global__ void __launch_bounds__(kStepWarps * 32) masked_step_kernel(const __gr
 
 namespace {
 
+// CTAs of one instance that the current device holds at once in clusters of
+// 2^log2s (a cluster lies within one of its groups of SMs, so that large ones
+// leave SMs over); asked once per device and size.  0: the size cannot run.
+template <int NB, bool BF, int NR, int WARPS>
+int step_slots(int log2s) {
+  static std::atomic<int> known[64][5] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = known[dev][log2s].load(std::memory_order_acquire);
+  if (n == 0) {
+    auto kern = masked_step_kernel<NB, BF, NR, WARPS>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1u << log2s);
+    cfg.blockDim = dim3(WARPS * 32);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 1u << log2s;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    // beyond 8 CTAs: not portable, but this device's
+    if (log2s > 3 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) n = -1;
+    if (n == 0 && (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1)) n = -1;
+    if (n < 0) cudaGetLastError();  // not an error of the call
+    n = n < 0 ? -1 : n << log2s;
+    known[dev][log2s].store(n, std::memory_order_release);
+  }
+  return n < 0 ? 0 : n;
+}
+
+template <int NB, bool BF, int NR, int WARPS>
+int launch_step_as(const StepParams& p, long long units, cudaStream_t st) {
+  return launch_pdl(masked_step_kernel<NB, BF, NR, WARPS>, dim3(static_cast<unsigned>(units * p.splits)),
+                    dim3(WARPS * 32), 0, st, p.splits, p) == cudaSuccess
+             ? JEPA_B200_OK
+             : JEPA_B200_ERR_CUDA;
+}
+
 template <int NB, bool BF, int NR>
 int launch_step(const MaskedAttnParams& a, cudaStream_t st) {
   StepParams p;
@@ -1293,27 +1366,32 @@ int launch_step(const MaskedAttnParams& a, cudaStream_t st) {
   const int rows = a.Nq * (a.hq / a.hk);
   p.chunks = (rows + 8 * NR - 1) / (8 * NR);
   const long long units = static_cast<long long>(a.B) * a.hk * p.chunks;
-  // Clusters as large as it takes to give every SM three CTAs, while a CTA
-  // keeps 256 keys, two tiles a warp.
+  if (units > 0x7fffffffll / 16) return JEPA_B200_ERR_SHAPE;
+  // The cluster size s and the warps w of a CTA that end first, by rounds of
+  // CTAs over the device times what one takes: its keys a warp, and a fixed
+  // part worth 40 + 8 s keys (about 14 keys a microsecond and warp; joining a
+  // cluster of 16 costs some 10 us).  16 x 8 key heads of 128 over 8192 keys:
+  // s w = 1 x 8 76 us, 2 x 4 76 us, 4 x 4 84 us, 8 x 4 106 us, 16 x 4 203 us.
+  double best = 1e30;
+  int warps = 4;
   p.splits = 1;
-  while (p.splits < 16 && units * p.splits < 3ll * num_sms() && a.Nk >= 2 * p.splits * 256) p.splits *= 2;
-  if (units * p.splits > 0x7fffffffll) return JEPA_B200_ERR_SHAPE;
-  auto kern = masked_step_kernel<NB, BF, NR>;
-  if (p.splits > 8) {  // beyond the portable size
-    static std::atomic<unsigned long long> done{0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return JEPA_B200_ERR_CUDA;
-    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-    if (!bit || !(done.load(std::memory_order_acquire) & bit)) {
-      if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-        return JEPA_B200_ERR_CUDA;
-      done.fetch_or(bit, std::memory_order_release);
+  for (int i = 0; i <= 4 && (i == 0 || a.Nk >= (2 * kStepKeys << i)); ++i)
+    for (int w = 4; w <= (NR == 1 ? 8 : 4); w *= 2) {
+      const int slots = w == 8 ? step_slots<NB, BF, 1, 8>(i) : step_slots<NB, BF, NR, 4>(i);
+      if (slots == 0) continue;
+      const int s = 1 << i;
+      const long long rounds = (units * s + slots - 1) / slots;
+      const double cost = static_cast<double>(rounds) * (static_cast<double>(a.Nk) / (s * w) + 40 + 8 * s);
+      if (cost < best) {
+        best = cost;
+        p.splits = s;
+        warps = w;
+      }
     }
+  if constexpr (NR == 1) {
+    if (warps == 8) return launch_step_as<NB, BF, 1, 8>(p, units, st);
   }
-  return launch_pdl(kern, dim3(static_cast<unsigned>(units * p.splits)), dim3(kStepWarps * 32), 0, st, p.splits, p) ==
-                 cudaSuccess
-             ? JEPA_B200_OK
-             : JEPA_B200_ERR_CUDA;
+  return launch_step_as<NB, BF, NR, 4>(p, units, st);
 }
 
 template <int NB, bool BF>
