@@ -457,6 +457,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __shared__ uint64_t q_full[kQBufs][2], q_empty[kQBufs][2];
   __shared__ uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   __shared__ uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], drain_bar[2];
+  __shared__ uint64_t item_full, item_empty, steal_bar;
+  __shared__ alignas(16) uint4 steal_answer;
+  __shared__ Item item_sh;  // the item that the CTA's warps turn to next; n < 0: none
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
 
@@ -484,6 +487,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     mbar_init(&drain_bar[0], 1);
     mbar_init(&drain_bar[1], 1);
+    mbar_init(&item_full, 1);
+    mbar_init(&item_empty, 1 + (C::kAliasP ? 1 : 2) + 8);  // TMA, MMA and softmax warps
+    mbar_init(&steal_bar, 1);
     abort_sh = 0;
     mbar_fence_init();
   }
@@ -509,11 +515,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (warp == 8) {
     // ---------------------------------------------------------------- TMA
     bool ok = true;
-    uint32_t kv = 0;             // key tiles loaded so far
+    uint32_t items = 0, kv = 0;  // items taken, key tiles loaded so far
     uint32_t qc[2] = {0, 0};     // Q tiles loaded so far
     uint32_t karmed = 0, varmed = 0;
-    for (int idx = blockIdx.x; ok && idx < p.n_items; idx += gridDim.x) {
-      const Item it = load_item(p, idx, lane);
+    while (ok) {
+      ok = warp_wait(&item_full, items++ & 1, w);
+      if (!ok) break;
+      const Item it = item_sh;
+      if (it.n < 0) break;
       if (lane == 0) {
         const int hk = it.h / (a.hq / a.hk);
         const int qb = (p.q_step & 1) ? it.b : 0, qh = (p.q_step & 4) ? it.h : 0;
@@ -555,6 +564,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       ok = __all_sync(0xffffffffu, ok);
+      // the next item is fetched once this one's loads are on their way: no
+      // earlier, since an item once taken stays with its CTA
+      if (lane == 0) mbar_arrive(&item_empty);
     }
     if (lane == 0) {  // whatever happened to the readers: the copies issued land before the CTA exits
       for (int g = 0; g < 2; ++g)
@@ -587,10 +599,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint64_t vdesc = sdesc_mnmajor_sw128(smem_u32(sm + C::kOffV), kBlockBytes);
     constexpr uint64_t kTile16 = C::kTileBytes / 16, kBlock16 = kBlockBytes / 16;  // descriptors count 16 bytes
     bool ok = true;
+    uint32_t items = 0;
     uint32_t ks = 0, kph = 0, vs = 0, vph = 0;        // stage and phase of the next K and V tile
     uint32_t qc[2] = {0, 0}, sc[2] = {0, 0}, pc[2] = {0, 0};  // Q tiles, S and P V products so far
-    for (int idx = blockIdx.x; ok && idx < p.n_items; idx += gridDim.x) {
-      const Item it = load_item(p, idx, lane);
+    while (ok) {
+      ok = warp_wait(&item_full, items++ & 1, w);
+      if (!ok) break;
+      const Item it = item_sh;
+      if (it.n < 0) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty);
       if (it.n == 0) continue;
       uint32_t buf[2];
 #pragma unroll
@@ -680,6 +698,36 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_wait_drain(&drain_bar[warp - 9], 0);
     }
     __syncwarp();
+  } else if (warp == 11) {
+    // -------------------------------------------------------------- items
+    // The CTA's own item, then those of CTAs that have not started: items
+    // differ in length (documents, causal rows), and this evens them out
+    // without a counter in memory.
+    int idx = static_cast<int>(blockIdx.x);
+    for (uint32_t n = 0;; ++n) {
+      Item it;
+      it.n = -1;
+      if (idx >= 0) it = load_item(p, idx, lane);
+      if (lane == 0) item_sh = it;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_full);
+      if (idx < 0) break;
+      // not before every warp has taken this one
+      if (!warp_wait(&item_empty, n & 1, w)) break;
+      if (lane == 0) {
+        fence_proxy_async_smem();
+        mbar_expect_tx(&steal_bar, 16);
+        clc_try_cancel(&steal_answer, &steal_bar);
+      }
+      __syncwarp();
+      if (!warp_wait(&steal_bar, n & 1, w)) {
+        mbar_wait_drain(&steal_bar, n & 1);
+        __syncwarp();
+        break;
+      }
+      idx = clc_cancelled(&steal_answer);
+    }
+    __syncwarp();
   }
   } else {
     regs_raise<kRegsSoftmax>();
@@ -693,9 +741,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     CapPoly<BF> cap;
     if constexpr ((MODE & kCap) != 0) cap.init(a.scale, a.cap);
     bool ok = true;
-    uint32_t cnt = 0, kv = 0;  // this tile's key tiles so far, the CTA's
-    for (int idx = blockIdx.x; ok && idx < p.n_items; idx += gridDim.x) {
-      const Item it = load_item(p, idx, lane);
+    uint32_t items = 0, cnt = 0, kv = 0;  // items taken, this tile's key tiles so far, the CTA's
+    while (ok) {
+      ok = warp_wait(&item_full, items++ & 1, w);
+      if (!ok) break;
+      const Item it = item_sh;
+      if (it.n < 0) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty);
       const int i = it.q0 + 128 * g + r;
       const bool row = i < a.Nq;
       RowKeys rk;
@@ -897,8 +950,7 @@ int launch_tiles(const TileParams& p, const CUtensorMap* tm, cudaStream_t st) {
   auto kern = masked_tiles_kernel<NB, BF, MODE>;
   static std::atomic<unsigned long long> attr_done{0};
   if (!smem_attr_once(attr_done, kern, C::kSmem)) return JEPA_B200_ERR_CUDA;
-  const int grid = p.n_items < num_sms() ? p.n_items : num_sms();
-  return launch_pdl(kern, dim3(grid), dim3(kTileThreads), C::kSmem, st, 1, tm[0], tm[1], tm[2], p) == cudaSuccess
+  return launch_pdl(kern, dim3(p.n_items), dim3(kTileThreads), C::kSmem, st, 1, tm[0], tm[1], tm[2], p) == cudaSuccess
              ? JEPA_B200_OK
              : JEPA_B200_ERR_CUDA;
 }
