@@ -321,14 +321,27 @@ __device__ __forceinline__ void finish_scores(float (&s)[128], const CapPoly<BF>
     }
   }
   if constexpr ((MODE & kBias) != 0) {
-    // slope * |p - j| as the magnitude of slope * (p - j), with the sign of -slope
-    const uint32_t sign = slope2 > 0.f ? 0x80000000u : 0u;
-    const float b0 = slope2 * dist0;
+    const bool left = __all_sync(0xffffffffu, dist0 >= 127.f), right = __all_sync(0xffffffffu, dist0 <= 0.f);
+    if (left || right) {
+      // every key of the tile on one side of every row: the bias is linear in the key
+      const float g = left ? slope2 : -slope2;
+      const uint64_t g2 = f2_pack(g, g), b2 = f2_pack(-g * dist0, -g * dist0), c2 = f2_pack(c, c);
 #pragma unroll
-    for (int e = 0; e < 128; ++e) {
-      const float t = fmaf(-slope2, static_cast<float>(e), b0);
-      const float bias = __uint_as_float((__float_as_uint(t) & 0x7fffffffu) | sign);
-      s[e] = (MODE & kCap) ? s[e] + bias : fmaf(s[e], c, bias);
+      for (int e = 0; e < 128; e += 2) {
+        const uint64_t v = f2_pack(s[e], s[e + 1]);
+        const uint64_t bias = f2_fma(f2_pack(static_cast<float>(e), static_cast<float>(e + 1)), g2, b2);
+        f2_unpack((MODE & kCap) ? f2_add(v, bias) : f2_fma(v, c2, bias), s[e], s[e + 1]);
+      }
+    } else {
+      // slope * |p - j| as the magnitude of slope * (p - j), with the sign of -slope
+      const uint32_t sign = slope2 > 0.f ? 0x80000000u : 0u;
+      const float b0 = slope2 * dist0;
+#pragma unroll
+      for (int e = 0; e < 128; ++e) {
+        const float t = fmaf(-slope2, static_cast<float>(e), b0);
+        const float bias = __uint_as_float((__float_as_uint(t) & 0x7fffffffu) | sign);
+        s[e] = (MODE & kCap) ? s[e] + bias : fmaf(s[e], c, bias);
+      }
     }
   } else if constexpr (MODE == 0) {
 #pragma unroll
@@ -883,20 +896,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       uint16_t* dst = a.out + it.b * a.o_b + static_cast<long long>(i) * a.o_n + it.h * a.o_h;
       float odd = 0.f;  // 0 unless a value of the row is not finite
 #pragma unroll 1
-      for (int t = 0; t < a.d; t += 16) {
-        uint32_t o[16];
-        if (some) tmem_ld16(tO + t, o);
-        uint32_t h[8];
+      for (int t = 0; t < a.d; t += 32) {
+        uint32_t o[32];
+        if (some) tmem_ld32(tO + t, o);
+        uint32_t h[16];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < 16; ++e) {
           const float x = some && full_row ? __uint_as_float(o[2 * e]) * inv : 0.f;
           const float y = some && full_row ? __uint_as_float(o[2 * e + 1]) * inv : 0.f;
-          odd = fmaf(x, 0.f, fmaf(y, 0.f, odd));
+          if (t + 2 * e < a.d) odd = fmaf(x, 0.f, fmaf(y, 0.f, odd));  // (columns behind the dims hold anything)
           h[e] = pack2<BF>(x, y);
         }
         if (row && rk.written) {
-          *reinterpret_cast<uint4*>(dst + t) = make_uint4(h[0], h[1], h[2], h[3]);
-          if (t + 8 < a.d) *reinterpret_cast<uint4*>(dst + t + 8) = make_uint4(h[4], h[5], h[6], h[7]);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (t + 8 * u < a.d)
+              *reinterpret_cast<uint4*>(dst + t + 8 * u) = make_uint4(h[4 * u], h[4 * u + 1], h[4 * u + 2], h[4 * u + 3]);
         }
       }
       // A value that is not finite may have come from a key that the row does
