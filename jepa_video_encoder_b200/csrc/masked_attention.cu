@@ -164,6 +164,8 @@ constexpr int kBlockBytes = 128 * 128;  // [128 rows x 64 dims] of 16 bits
 // Score transforms of a kernel instance.
 constexpr int kCap = 1, kBias = 2;
 
+constexpr int kOutBytes = 32 * 128;
+
 template <int NB>  // 64-dim blocks of a head: 1 or 2
 struct TileCfg {
   static constexpr int kStages = NB == 1 ? 4 : 2;
@@ -172,7 +174,8 @@ struct TileCfg {
   static constexpr int kOffQ = 0;  // [buffer][tile]
   static constexpr int kOffK = kOffQ + kQBufs * 2 * kTileBytes;
   static constexpr int kOffV = kOffK + kStages * kTileBytes;
-  static constexpr int kSmem = kOffV + kStages * kTileBytes + 1024;
+  static constexpr int kOffOut = kOffV + kStages * kTileBytes;  // [softmax warp] 32 rows of 64 dims on their way out
+  static constexpr int kSmem = kOffOut + 8 * kOutBytes + 1024;
   static constexpr bool kAliasP = NB == 2;
   static constexpr uint32_t kColS = 0, kColO = 256, kColP = NB == 1 ? 384 : 0;
   static constexpr uint32_t kStepO = 64 * NB, kStepP = NB == 1 ? 64 : 128;
@@ -185,7 +188,7 @@ constexpr int kRegsSoftmax = 224, kRegsOther = 56;
 struct TileParams {
   MaskedAttnParams a;
   int n_pairs, n_items;        // 256-row groups of a head; items = B * hq * n_pairs
-  int q_step, k_step, v_step;  // bit 0: batch, bit 1: token, bit 2: head axis has a stride (0: broadcast)
+  int q_step, k_step, v_step, o_step;  // bit 0: batch, bit 1: token, bit 2: head axis has a stride (0: broadcast)
 };
 
 // The key tiles of one item: tile j holds keys lo + 128 j ..; query tile g
@@ -463,7 +466,8 @@ constexpr int kPolyPairs = MODE == 0 ? 4 : (MODE == kBias ? 3 : 0);
 template <int NB, bool BF, int MODE>
 __global__ void __launch_bounds__(kTileThreads, 1)
     masked_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TileParams p) {
+                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                        const __grid_constant__ TileParams p) {
   using C = TileCfg<NB>;
   constexpr int kStages = C::kStages, kQBufs = C::kQBufs;
   extern __shared__ uint8_t dsmem[];
@@ -893,31 +897,59 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       tc_fence_after();
       const bool full_row = rk.hi > rk.lo;
       const float inv = full_row ? 1.0f / l_run : 0.f;
+      // The rows go out through shared memory and TMA, 64 dims at a time: a
+      // store instruction over 32 rows of their own took 32 passes, 2000 to
+      // 4000 clocks an item.  Where a row must be left as it is (no document),
+      // each thread stores its own.
       uint16_t* dst = a.out + it.b * a.o_b + static_cast<long long>(i) * a.o_n + it.h * a.o_h;
+      uint8_t* stage = sm + C::kOffOut + warp * kOutBytes;
+      const bool by_tma = __all_sync(0xffffffffu, !row || rk.written);
+      const int row0 = it.q0 + 128 * g + quad * 32;  // the warp's first row
       float odd = 0.f;  // 0 unless a value of the row is not finite
 #pragma unroll 1
-      for (int t = 0; t < a.d; t += 32) {
-        uint32_t o[32];
-        if (some) tmem_ld32(tO + t, o);
-        uint32_t h[16];
+      for (int blk = 0; 64 * blk < a.d; ++blk) {
+        if (lane == 0) bulk_wait_read0();  // the rows staged before have been read
+        __syncwarp();
+#pragma unroll 1
+        for (int t = 64 * blk; t < min(a.d, 64 * blk + 64); t += 32) {
+          uint32_t o[32];
+          if (some) tmem_ld32(tO + t, o);
+          uint32_t h[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float x = some && full_row ? __uint_as_float(o[2 * e]) * inv : 0.f;
-          const float y = some && full_row ? __uint_as_float(o[2 * e + 1]) * inv : 0.f;
-          if (t + 2 * e < a.d) odd = fmaf(x, 0.f, fmaf(y, 0.f, odd));  // (columns behind the dims hold anything)
-          h[e] = pack2<BF>(x, y);
-        }
-        if (row && rk.written) {
+          for (int e = 0; e < 16; ++e) {
+            const float x = some && full_row ? __uint_as_float(o[2 * e]) * inv : 0.f;
+            const float y = some && full_row ? __uint_as_float(o[2 * e + 1]) * inv : 0.f;
+            if (t + 2 * e < a.d) odd = fmaf(x, 0.f, fmaf(y, 0.f, odd));  // (columns behind the dims hold anything)
+            h[e] = pack2<BF>(x, y);
+          }
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (t + 8 * u < a.d)
+          for (int u = 0; u < 4; ++u) {
+            if (by_tma)
+              st_shared_v4(smem_u32(stage) + sw128_offset(lane, (t & 32) + 8 * u), h[4 * u], h[4 * u + 1], h[4 * u + 2],
+                           h[4 * u + 3]);
+            else if (row && rk.written && t + 8 * u < a.d)
               *reinterpret_cast<uint4*>(dst + t + 8 * u) = make_uint4(h[4 * u], h[4 * u + 1], h[4 * u + 2], h[4 * u + 3]);
+          }
+        }
+        if (by_tma && row0 < a.Nq) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_4d(&tmO, stage, 64 * blk, (p.o_step & 4) ? it.h : 0, row0, (p.o_step & 1) ? it.b : 0);
+            bulk_commit();
+          }
         }
       }
       // A value that is not finite may have come from a key that the row does
-      // not read (0 * inf in the tile's product): such rows anew, by the
+      // not read (0 * inf in the tile's product), and a row whose scores are all
+      // -inf has nothing but the polynomial's 2^-126: such rows anew, by the
       // definition.
-      unsigned again = __ballot_sync(0xffffffffu, row && rk.written && full_row && !(odd == 0.f));
+      unsigned again =
+          __ballot_sync(0xffffffffu, row && rk.written && full_row && (!(odd == 0.f) || m_run == -INFINITY));
+      if (again) {  // (not before the rows written above have landed)
+        if (lane == 0) bulk_wait0();
+        __syncwarp();
+      }
       while (again) {
         const int src = __ffs(again) - 1;
         again &= again - 1;
@@ -931,6 +963,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       tc_fence_before();
     }
     tmem_wait_ld();  // nothing in flight when the columns are given back
+    if (lane == 0) bulk_wait0();
   }
   tc_fence_before();
   __syncthreads();
@@ -942,11 +975,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
 namespace {
 
-// [B, N, heads, d] as a map of (d, heads, N, B) with tiles of 128 tokens by 64
-// dims, zeros outside; an axis without a stride has length 1.  Returns the
+// [B, N, heads, d] as a map of (d, heads, N, B) with tiles of `rows` tokens by
+// 64 dims, zeros outside; an axis without a stride has length 1.  Returns the
 // axes that have one (TileParams::q_step).
 bool make_tile_map(CUtensorMap* m, const uint16_t* data, int d, int H, int N, int B, long long sh, long long sn,
-                   long long sb, int* step) {
+                   long long sb, int rows, int* step) {
   const bool hb = B > 1 && sb > 0, hh = H > 1 && sh > 0, hn = N > 1 && sn > 0;
   if (N > 1 && !hn) return false;
   const uint64_t dims[4] = {static_cast<uint64_t>(d), hh ? static_cast<uint64_t>(H) : 1u, static_cast<uint64_t>(N),
@@ -954,7 +987,7 @@ bool make_tile_map(CUtensorMap* m, const uint16_t* data, int d, int H, int N, in
   const uint64_t one = static_cast<uint64_t>(d) * 2;
   const uint64_t str[3] = {hh ? static_cast<uint64_t>(sh) * 2 : one, hn ? static_cast<uint64_t>(sn) * 2 : one,
                            hb ? static_cast<uint64_t>(sb) * 2 : one};
-  const uint32_t box[4] = {64, 1, 128, 1};
+  const uint32_t box[4] = {64, 1, static_cast<uint32_t>(rows), 1};
   *step = (hb ? 1 : 0) | (hn ? 2 : 0) | (hh ? 4 : 0);
   return make_tmap_f16(m, data, 4, dims, str, box);
 }
@@ -965,7 +998,7 @@ int launch_tiles(const TileParams& p, const CUtensorMap* tm, cudaStream_t st) {
   auto kern = masked_tiles_kernel<NB, BF, MODE>;
   static std::atomic<unsigned long long> attr_done{0};
   if (!smem_attr_once(attr_done, kern, C::kSmem)) return JEPA_B200_ERR_CUDA;
-  return launch_pdl(kern, dim3(p.n_items), dim3(kTileThreads), C::kSmem, st, 1, tm[0], tm[1], tm[2], p) == cudaSuccess
+  return launch_pdl(kern, dim3(p.n_items), dim3(kTileThreads), C::kSmem, st, 1, tm[0], tm[1], tm[2], tm[3], p) == cudaSuccess
              ? JEPA_B200_OK
              : JEPA_B200_ERR_CUDA;
 }
@@ -1493,10 +1526,11 @@ int launch_masked_attention(const MaskedAttnParams& p, bool bf16, cudaStream_t s
     const long long items = static_cast<long long>(p.B) * p.hq * tp.n_pairs;
     if (items > 0x7fffffffll) return JEPA_B200_ERR_SHAPE;
     tp.n_items = static_cast<int>(items);
-    CUtensorMap tm[3];
-    if (p.Nk > 0 && make_tile_map(&tm[0], p.q, p.d, p.hq, p.Nq, p.B, p.q_h, p.q_n, p.q_b, &tp.q_step) &&
-        make_tile_map(&tm[1], p.k, p.d, p.hk, p.Nk, p.B, p.k_h, p.k_n, p.k_b, &tp.k_step) &&
-        make_tile_map(&tm[2], p.v, p.d, p.hk, p.Nk, p.B, p.v_h, p.v_n, p.v_b, &tp.v_step)) {
+    CUtensorMap tm[4];
+    if (p.Nk > 0 && make_tile_map(&tm[0], p.q, p.d, p.hq, p.Nq, p.B, p.q_h, p.q_n, p.q_b, 128, &tp.q_step) &&
+        make_tile_map(&tm[1], p.k, p.d, p.hk, p.Nk, p.B, p.k_h, p.k_n, p.k_b, 128, &tp.k_step) &&
+        make_tile_map(&tm[2], p.v, p.d, p.hk, p.Nk, p.B, p.v_h, p.v_n, p.v_b, 128, &tp.v_step) &&
+        make_tile_map(&tm[3], p.out, p.d, p.hq, p.Nq, p.B, p.o_h, p.o_n, p.o_b, 32, &tp.o_step)) {
       if (p.d <= 64) return bf16 ? launch_tiles_mode<1, true>(tp, tm, st) : launch_tiles_mode<1, false>(tp, tm, st);
       return bf16 ? launch_tiles_mode<2, true>(tp, tm, st) : launch_tiles_mode<2, false>(tp, tm, st);
     }

@@ -548,6 +548,94 @@ def test_attention_values_that_are_read_arrive():
         _ok()
 
 
+@pytest.mark.parametrize("Nq", [2, 200])
+@pytest.mark.parametrize("dtype,d", [(torch.float16, 64), (torch.bfloat16, 128)])
+def test_attention_scores_of_minus_infinity(Nq, dtype, d):
+    """A row whose every allowed score is -inf is 0 / 0; one score of -inf
+    beside finite ones counts nothing."""
+    need_cuda()
+    q, k, v = _qkv(12, 1, Nq, 200, 1, 1, d, dtype)
+    q = q.abs() + 0.5
+    k[0, :, 0] = 0
+    k[0, 100:, 0, 0] = -float("inf")
+    got = jb.masked_attention(q, k, v, kv_len=_ints([150]))
+    want, tol = ref_attention(q, torch.where(torch.isfinite(k), k, 0), v, 1 / math.sqrt(d),
+                              allowed=allow(1, Nq, 200, kv_len=[100])[0])
+    assert ((got.double() - want).abs() <= tol).all()
+    k[0, :, 0, 0] = -float("inf")
+    assert torch.isnan(jb.masked_attention(q, k, v, kv_len=_ints([150]))).all()
+    _ok()
+
+
+@pytest.mark.parametrize("causal,docs", [(True, False), (False, True), (False, False)])
+@pytest.mark.parametrize("dtype,d", [(torch.float16, 64), (torch.bfloat16, 96)])
+def test_attention_more_work_than_the_device_holds(causal, docs, dtype, d):
+    """More pieces of work than SMs, of unequal lengths: every one is done,
+    once, whichever CTA takes it."""
+    need_cuda()
+    B, N, h = 5, 700, 16
+    q, k, v = _qkv(13, B, N, N, h, h, d, dtype)
+    rng = np.random.default_rng(2)
+    off = [[0] + sorted(rng.choice(np.arange(1, N), 5, replace=False).tolist()) + [N] for _ in range(B)]
+    mask = dict(causal=causal) | (dict(docs=off) if docs else {})
+    got, _ = check_attention(q, k, v, mask=mask)
+    call = dict(causal=causal, doc_offsets=_ints(off) if docs else None)
+    for _ in range(5):
+        out = torch.full_like(q, float("nan"))
+        assert torch.equal(jb.masked_attention(q, k, v, out=out, **call), got)
+    _ok()
+
+
+def test_attention_wait_bound():
+    """A bound of 0 makes the first wait that is not over give up: the call
+    unwinds, the status says so, and the next call works."""
+    need_cuda()
+    q, k, v = _qkv(14, 3, 600, 600, 32, 32, 64, torch.float16)
+    want = jb.masked_attention(q, k, v)
+    _ok()
+    jb.op_set_timeout_ns(0)
+    jb.masked_attention(q, k, v)
+    st = jb.op_sync_status()
+    jb.op_set_timeout_ns(4_000_000_000)
+    assert st == jb._abi.ERR_TIMEOUT
+    _ok()
+    assert torch.equal(jb.masked_attention(q, k, v), want)
+    _ok()
+
+
+FIRST_CALL = """
+import torch
+import jepa_video_encoder_b200 as jb
+q = torch.ones(2, {Nq}, 4, 64, dtype=torch.float16, device="cuda")
+k = torch.ones(2, 900, 4, 64, dtype=torch.float16, device="cuda")
+plan = jb.rope_plan(64)
+pos = torch.arange({Nq}, device="cuda")
+w = torch.ones(64, device="cuda")
+out = torch.zeros_like(q)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    a, b = jb.qk_norm_rope(q, jb.rope(q, pos, plan), pos, plan, w, w)
+    jb.masked_attention(a, k, k, causal=True, out=out)
+g.replay()
+torch.cuda.synchronize()
+assert jb.op_sync_status() == 0
+assert (out == 1).all(), out
+"""
+
+
+@pytest.mark.parametrize("Nq", [1, 900])
+def test_first_call_of_a_process_captured(Nq):
+    """Nothing needs a warm-up call outside the capture."""
+    need_cuda()
+    import os
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL.format(Nq=Nq)], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 @pytest.mark.parametrize("Nq,Nk", [(200, 200), (2, 200)])
 @pytest.mark.parametrize("how", ["fused", "heads_first", "broadcast_batch", "broadcast_head", "padded_rows", "reversed_layout"])
 def test_attention_strides(Nq, Nk, how):
