@@ -476,7 +476,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __shared__ uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], drain_bar[2];
   __shared__ uint64_t item_full, item_empty, steal_bar;
   __shared__ alignas(16) uint4 steal_answer;
-  __shared__ Item item_sh;  // the item that the CTA's warps turn to next; n < 0: none
+  // The item that the CTA's warps are at, and the next; n < 0: none.  A slot is
+  // written again only when every warp has taken the item behind it.
+  __shared__ Item item_sh[2];
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
 
@@ -528,224 +530,224 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   w.where = (KID_ATTN << 8) | static_cast<unsigned>(warp);
 
   if (warp >= 8) {
-  regs_lower<kRegsOther>();
-  if (warp == 8) {
-    // ---------------------------------------------------------------- TMA
-    bool ok = true;
-    uint32_t items = 0, kv = 0;  // items taken, key tiles loaded so far
-    uint32_t qc[2] = {0, 0};     // Q tiles loaded so far
-    uint32_t karmed = 0, varmed = 0;
-    while (ok) {
-      ok = warp_wait(&item_full, items++ & 1, w);
-      if (!ok) break;
-      const Item it = item_sh;
-      if (it.n < 0) break;
-      if (lane == 0) {
-        const int hk = it.h / (a.hq / a.hk);
-        const int qb = (p.q_step & 1) ? it.b : 0, qh = (p.q_step & 4) ? it.h : 0;
-        const int kb = (p.k_step & 1) ? it.b : 0, kh = (p.k_step & 4) ? hk : 0;
-        const int vb = (p.v_step & 1) ? it.b : 0, vh = (p.v_step & 4) ? hk : 0;
-        for (int g = 0; ok && g < 2; ++g) {
-          if (it.last[g] == 0) continue;
-          const int buf = static_cast<int>(qc[g] % kQBufs);
-          if (!sleep_wait(&q_empty[buf][g], ((qc[g] / kQBufs) & 1) ^ 1, w)) {
-            ok = false;
-            break;
+    regs_lower<kRegsOther>();
+    if (warp == 8) {
+      // ---------------------------------------------------------------- TMA
+      bool ok = true;
+      uint32_t items = 0, kv = 0;  // items taken, key tiles loaded so far
+      uint32_t qc[2] = {0, 0};     // Q tiles loaded so far
+      uint32_t karmed = 0, varmed = 0;
+      while (ok) {
+        ok = warp_wait(&item_full, items & 1, w);
+        if (!ok) break;
+        const Item it = item_sh[items++ & 1];
+        if (it.n < 0) break;
+        if (lane == 0) {
+          const int hk = it.h / (a.hq / a.hk);
+          const int qb = (p.q_step & 1) ? it.b : 0, qh = (p.q_step & 4) ? it.h : 0;
+          const int kb = (p.k_step & 1) ? it.b : 0, kh = (p.k_step & 4) ? hk : 0;
+          const int vb = (p.v_step & 1) ? it.b : 0, vh = (p.v_step & 4) ? hk : 0;
+          for (int g = 0; ok && g < 2; ++g) {
+            if (it.last[g] == 0) continue;
+            const int buf = static_cast<int>(qc[g] % kQBufs);
+            if (!sleep_wait(&q_empty[buf][g], ((qc[g] / kQBufs) & 1) ^ 1, w)) {
+              ok = false;
+              break;
+            }
+            mbar_expect_tx(&q_full[buf][g], C::kTileBytes);
+            for (int c = 0; c < NB; ++c)
+              tma_load_4d(sm + C::kOffQ + (buf * 2 + g) * C::kTileBytes + c * kBlockBytes, &tmQ, &q_full[buf][g], 64 * c,
+                          qh, it.q0 + 128 * g, qb);
+            ++qc[g];
           }
-          mbar_expect_tx(&q_full[buf][g], C::kTileBytes);
-          for (int c = 0; c < NB; ++c)
-            tma_load_4d(sm + C::kOffQ + (buf * 2 + g) * C::kTileBytes + c * kBlockBytes, &tmQ, &q_full[buf][g], 64 * c,
-                        qh, it.q0 + 128 * g, qb);
-          ++qc[g];
+          for (int j = 0; ok && j < it.n; ++j, ++kv) {
+            const int s = static_cast<int>(kv % kStages);
+            const uint32_t ph = (kv / kStages) & 1;
+            const int key = it.lo + 128 * j;
+            if (!sleep_wait(&k_empty[s], ph ^ 1, w)) {
+              ok = false;
+              break;
+            }
+            mbar_expect_tx(&k_full[s], C::kTileBytes);
+            for (int c = 0; c < NB; ++c)
+              tma_load_4d(sm + C::kOffK + s * C::kTileBytes + c * kBlockBytes, &tmK, &k_full[s], 64 * c, kh, key, kb);
+            karmed = (karmed & ~(3u << (2 * s))) | ((1u | (ph << 1)) << (2 * s));
+            if (!sleep_wait(&v_empty[s], ph ^ 1, w)) {
+              ok = false;
+              break;
+            }
+            mbar_expect_tx(&v_full[s], C::kTileBytes);
+            for (int c = 0; c < NB; ++c)
+              tma_load_4d(sm + C::kOffV + s * C::kTileBytes + c * kBlockBytes, &tmV, &v_full[s], 64 * c, vh, key, vb);
+            varmed = (varmed & ~(3u << (2 * s))) | ((1u | (ph << 1)) << (2 * s));
+          }
         }
-        for (int j = 0; ok && j < it.n; ++j, ++kv) {
-          const int s = static_cast<int>(kv % kStages);
-          const uint32_t ph = (kv / kStages) & 1;
-          const int key = it.lo + 128 * j;
-          if (!sleep_wait(&k_empty[s], ph ^ 1, w)) {
-            ok = false;
-            break;
-          }
-          mbar_expect_tx(&k_full[s], C::kTileBytes);
-          for (int c = 0; c < NB; ++c)
-            tma_load_4d(sm + C::kOffK + s * C::kTileBytes + c * kBlockBytes, &tmK, &k_full[s], 64 * c, kh, key, kb);
-          karmed = (karmed & ~(3u << (2 * s))) | ((1u | (ph << 1)) << (2 * s));
-          if (!sleep_wait(&v_empty[s], ph ^ 1, w)) {
-            ok = false;
-            break;
-          }
-          mbar_expect_tx(&v_full[s], C::kTileBytes);
-          for (int c = 0; c < NB; ++c)
-            tma_load_4d(sm + C::kOffV + s * C::kTileBytes + c * kBlockBytes, &tmV, &v_full[s], 64 * c, vh, key, vb);
-          varmed = (varmed & ~(3u << (2 * s))) | ((1u | (ph << 1)) << (2 * s));
+        ok = __all_sync(0xffffffffu, ok);
+        // the next item is fetched once this one's loads are on their way: no
+        // earlier, since an item once taken stays with its CTA
+        if (lane == 0) mbar_arrive(&item_empty);
+      }
+      if (lane == 0) {  // whatever happened to the readers: the copies issued land before the CTA exits
+        for (int g = 0; g < 2; ++g)
+          for (uint32_t i = 0; i < kQBufs; ++i)
+            if (qc[g] > i) {
+              const uint32_t last = qc[g] - 1 - i;
+              mbar_wait_drain(&q_full[last % kQBufs][g], (last / kQBufs) & 1);
+            }
+        for (int s = 0; s < kStages; ++s) {
+          if ((karmed >> (2 * s)) & 1u) mbar_wait_drain(&k_full[s], (karmed >> (2 * s + 1)) & 1u);
+          if ((varmed >> (2 * s)) & 1u) mbar_wait_drain(&v_full[s], (varmed >> (2 * s + 1)) & 1u);
         }
       }
-      ok = __all_sync(0xffffffffu, ok);
-      // the next item is fetched once this one's loads are on their way: no
-      // earlier, since an item once taken stays with its CTA
-      if (lane == 0) mbar_arrive(&item_empty);
-    }
-    if (lane == 0) {  // whatever happened to the readers: the copies issued land before the CTA exits
-      for (int g = 0; g < 2; ++g)
-        for (uint32_t i = 0; i < kQBufs; ++i)
-          if (qc[g] > i) {
-            const uint32_t last = qc[g] - 1 - i;
-            mbar_wait_drain(&q_full[last % kQBufs][g], (last / kQBufs) & 1);
+    } else if (warp == 9 || (warp == 10 && !C::kAliasP)) {
+      // ---------------------------------------------------------------- MMA
+      // Both query tiles in a fixed turn: the tensor core works for one tile
+      // while the other is in its softmax.  P beside S: warp 9 issues S and warp
+      // 10 P V, each at its own pace.  P in S's place: warp 9 issues P V and the
+      // S that follows it, in order.  The whole warp walks
+      // the loop and one elected lane issues, on descriptors that differ by
+      // constants: operands then stay in uniform registers (a lane's own branch
+      // issues a 128 x 64 x 16 product every 60 to 104 clocks, this one every
+      // 32, the tensor core's own pace).
+      const bool lead = elect_one();
+      const uint32_t idesc_s = idesc_f16_f32(128, 128, BF);
+      const int ksteps = (a.d + 15) >> 4;  // 16 dims each: zeros behind d
+      const uint32_t idesc_o = idesc_f16_f32(128, 16 * ksteps, BF) | kIdescBMnMajor;
+      const uint64_t qdesc = sdesc_kmajor_sw128(smem_u32(sm + C::kOffQ));
+      const uint64_t kdesc = sdesc_kmajor_sw128(smem_u32(sm + C::kOffK));
+      const uint64_t vdesc = sdesc_mnmajor_sw128(smem_u32(sm + C::kOffV), kBlockBytes);
+      constexpr uint64_t kTile16 = C::kTileBytes / 16, kBlock16 = kBlockBytes / 16;  // descriptors count 16 bytes
+      bool ok = true;
+      uint32_t items = 0;
+      uint32_t ks = 0, kph = 0, vs = 0, vph = 0;        // stage and phase of the next K and V tile
+      uint32_t qc[2] = {0, 0}, sc[2] = {0, 0}, pc[2] = {0, 0};  // Q tiles, S and P V products so far
+      while (ok) {
+        ok = warp_wait(&item_full, items & 1, w);
+        if (!ok) break;
+        const Item it = item_sh[items++ & 1];
+        if (it.n < 0) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&item_empty);
+        if (it.n == 0) continue;
+        uint32_t buf[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          buf[g] = qc[g] % kQBufs;
+          if (it.last[g] > 0 && warp == 9) {
+            ok = ok && warp_wait(&q_full[buf[g]][g], (qc[g] / kQBufs) & 1, w);
+            ++qc[g];
           }
-      for (int s = 0; s < kStages; ++s) {
-        if ((karmed >> (2 * s)) & 1u) mbar_wait_drain(&k_full[s], (karmed >> (2 * s + 1)) & 1u);
-        if ((varmed >> (2 * s)) & 1u) mbar_wait_drain(&v_full[s], (varmed >> (2 * s + 1)) & 1u);
-      }
-    }
-  } else if (warp == 9 || (warp == 10 && !C::kAliasP)) {
-    // ---------------------------------------------------------------- MMA
-    // Both query tiles in a fixed turn: the tensor core works for one tile
-    // while the other is in its softmax.  P beside S: warp 9 issues S and warp
-    // 10 P V, each at its own pace.  P in S's place: warp 9 issues P V and the
-    // S that follows it, in order.  The whole warp walks
-    // the loop and one elected lane issues, on descriptors that differ by
-    // constants: operands then stay in uniform registers (a lane's own branch
-    // issues a 128 x 64 x 16 product every 60 to 104 clocks, this one every
-    // 32, the tensor core's own pace).
-    const bool lead = elect_one();
-    const uint32_t idesc_s = idesc_f16_f32(128, 128, BF);
-    const int ksteps = (a.d + 15) >> 4;  // 16 dims each: zeros behind d
-    const uint32_t idesc_o = idesc_f16_f32(128, 16 * ksteps, BF) | kIdescBMnMajor;
-    const uint64_t qdesc = sdesc_kmajor_sw128(smem_u32(sm + C::kOffQ));
-    const uint64_t kdesc = sdesc_kmajor_sw128(smem_u32(sm + C::kOffK));
-    const uint64_t vdesc = sdesc_mnmajor_sw128(smem_u32(sm + C::kOffV), kBlockBytes);
-    constexpr uint64_t kTile16 = C::kTileBytes / 16, kBlock16 = kBlockBytes / 16;  // descriptors count 16 bytes
-    bool ok = true;
-    uint32_t items = 0;
-    uint32_t ks = 0, kph = 0, vs = 0, vph = 0;        // stage and phase of the next K and V tile
-    uint32_t qc[2] = {0, 0}, sc[2] = {0, 0}, pc[2] = {0, 0};  // Q tiles, S and P V products so far
-    while (ok) {
-      ok = warp_wait(&item_full, items++ & 1, w);
-      if (!ok) break;
-      const Item it = item_sh;
-      if (it.n < 0) break;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&item_empty);
-      if (it.n == 0) continue;
-      uint32_t buf[2];
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        buf[g] = qc[g] % kQBufs;
-        if (it.last[g] > 0 && warp == 9) {
-          ok = ok && warp_wait(&q_full[buf[g]][g], (qc[g] / kQBufs) & 1, w);
-          ++qc[g];
         }
-      }
-      // S of key tile j
-      const auto issue_s = [&](int j, int g) {
-        if (j < it.first[g] || j >= it.last[g]) return true;
-        // P beside S: S may be overwritten once the softmax has taken the tile
-        // before; P in S's place: the product that reads it was issued before
-        if (!C::kAliasP && sc[g] > 0 && !warp_wait(&s_free[g], (sc[g] - 1) & 1, w)) return false;
-        ++sc[g];
-        tc_fence_after();
-        const uint64_t qd = qdesc + (buf[g] * 2 + g) * kTile16, kd = kdesc + ks * kTile16;
-        if (lead) {
+        // S of key tile j
+        const auto issue_s = [&](int j, int g) {
+          if (j < it.first[g] || j >= it.last[g]) return true;
+          // P beside S: S may be overwritten once the softmax has taken the tile
+          // before; P in S's place: the product that reads it was issued before
+          if (!C::kAliasP && sc[g] > 0 && !warp_wait(&s_free[g], (sc[g] - 1) & 1, w)) return false;
+          ++sc[g];
+          tc_fence_after();
+          const uint64_t qd = qdesc + (buf[g] * 2 + g) * kTile16, kd = kdesc + ks * kTile16;
+          if (lead) {
 #pragma unroll
-          for (int t = 0; t < 4 * NB; ++t)
-            if (t < ksteps)
-              tc_mma_f16_ss(tmem + C::kColS + 128 * g, qd + (t >> 2) * kBlock16 + (t & 3) * 2,
-                            kd + (t >> 2) * kBlock16 + (t & 3) * 2, idesc_s, t > 0 ? 1u : 0u);
-          tc_commit(&s_full[g]);
-          if (j == it.last[g] - 1) tc_commit(&q_empty[buf[g]][g]);
-        }
-        return true;
-      };
-      // O += P V of key tile j
-      const auto issue_pv = [&](int j, int g) {
-        if (j < it.first[g] || j >= it.last[g]) return true;
-        if (!warp_wait(&p_full[g], pc[g] & 1, w)) return false;
-        ++pc[g];
-        tc_fence_after();
-        const uint64_t vd = vdesc + vs * kTile16;
-        if (lead) {
+            for (int t = 0; t < 4 * NB; ++t)
+              if (t < ksteps)
+                tc_mma_f16_ss(tmem + C::kColS + 128 * g, qd + (t >> 2) * kBlock16 + (t & 3) * 2,
+                              kd + (t >> 2) * kBlock16 + (t & 3) * 2, idesc_s, t > 0 ? 1u : 0u);
+            tc_commit(&s_full[g]);
+            if (j == it.last[g] - 1) tc_commit(&q_empty[buf[g]][g]);
+          }
+          return true;
+        };
+        // O += P V of key tile j
+        const auto issue_pv = [&](int j, int g) {
+          if (j < it.first[g] || j >= it.last[g]) return true;
+          if (!warp_wait(&p_full[g], pc[g] & 1, w)) return false;
+          ++pc[g];
+          tc_fence_after();
+          const uint64_t vd = vdesc + vs * kTile16;
+          if (lead) {
 #pragma unroll
-          for (int t = 0; t < 8; ++t)  // 16 keys each
-            tc_mma_f16_ts(tmem + C::kColO + C::kStepO * g, tmem + C::kColP + C::kStepP * g + 8 * t, vd + t * 128,
-                          idesc_o, (j > it.first[g] || t > 0) ? 1u : 0u);
-          tc_commit(&pv_done[g]);
-        }
-        return true;
-      };
-      const auto k_release = [&] {
-        if (lead) tc_commit(&k_empty[ks]);
-        if (++ks == kStages) ks = 0, kph ^= 1;
-      };
-      const auto v_release = [&] {
-        if (lead) tc_commit(&v_empty[vs]);
-        if (++vs == kStages) vs = 0, vph ^= 1;
-      };
-      if constexpr (!C::kAliasP) {
-        if (warp == 9) {
-          for (int j = 0; ok && j < it.n; ++j) {
-            ok = warp_wait(&k_full[ks], kph, w) && issue_s(j, 0) && issue_s(j, 1);
-            if (ok) k_release();
+            for (int t = 0; t < 8; ++t)  // 16 keys each
+              tc_mma_f16_ts(tmem + C::kColO + C::kStepO * g, tmem + C::kColP + C::kStepP * g + 8 * t, vd + t * 128,
+                            idesc_o, (j > it.first[g] || t > 0) ? 1u : 0u);
+            tc_commit(&pv_done[g]);
+          }
+          return true;
+        };
+        const auto k_release = [&] {
+          if (lead) tc_commit(&k_empty[ks]);
+          if (++ks == kStages) ks = 0, kph ^= 1;
+        };
+        const auto v_release = [&] {
+          if (lead) tc_commit(&v_empty[vs]);
+          if (++vs == kStages) vs = 0, vph ^= 1;
+        };
+        if constexpr (!C::kAliasP) {
+          if (warp == 9) {
+            for (int j = 0; ok && j < it.n; ++j) {
+              ok = warp_wait(&k_full[ks], kph, w) && issue_s(j, 0) && issue_s(j, 1);
+              if (ok) k_release();
+            }
+          } else {
+            for (int j = 0; ok && j < it.n; ++j) {
+              ok = warp_wait(&v_full[vs], vph, w) && issue_pv(j, 0) && issue_pv(j, 1);
+              if (ok) v_release();
+            }
           }
         } else {
+          ok = ok && warp_wait(&k_full[ks], kph, w) && issue_s(0, 0) && issue_s(0, 1);
+          if (ok) k_release();
           for (int j = 0; ok && j < it.n; ++j) {
-            ok = warp_wait(&v_full[vs], vph, w) && issue_pv(j, 0) && issue_pv(j, 1);
-            if (ok) v_release();
-          }
-        }
-      } else {
-        ok = ok && warp_wait(&k_full[ks], kph, w) && issue_s(0, 0) && issue_s(0, 1);
-        if (ok) k_release();
-        for (int j = 0; ok && j < it.n; ++j) {
-          const bool more = j + 1 < it.n;
-          if (more) ok = warp_wait(&k_full[ks], kph, w);
-          ok = ok && warp_wait(&v_full[vs], vph, w);
+            const bool more = j + 1 < it.n;
+            if (more) ok = warp_wait(&k_full[ks], kph, w);
+            ok = ok && warp_wait(&v_full[vs], vph, w);
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            ok = ok && issue_pv(j, g);
-            if (more) ok = ok && issue_s(j + 1, g);
+            for (int g = 0; g < 2; ++g) {
+              ok = ok && issue_pv(j, g);
+              if (more) ok = ok && issue_s(j + 1, g);
+            }
+            if (!ok) break;
+            v_release();
+            if (more) k_release();
           }
-          if (!ok) break;
-          v_release();
-          if (more) k_release();
         }
       }
-    }
-    if (lead) {
-      tc_commit(&drain_bar[warp - 9]);
-      mbar_wait_drain(&drain_bar[warp - 9], 0);
-    }
-    __syncwarp();
-  } else if (warp == 11) {
-    // -------------------------------------------------------------- items
-    // The CTA's own item, then those of CTAs that have not started: items
-    // differ in length (documents, causal rows), and this evens them out
-    // without a counter in memory.
-    int idx = static_cast<int>(blockIdx.x);
-    for (uint32_t n = 0;; ++n) {
-      Item it;
-      it.n = -1;
-      if (idx >= 0) it = load_item(p, idx, lane);
-      if (lane == 0) item_sh = it;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&item_full);
-      if (idx < 0) break;
-      // not before every warp has taken this one
-      if (!warp_wait(&item_empty, n & 1, w)) break;
-      if (lane == 0) {
-        fence_proxy_async_smem();
-        mbar_expect_tx(&steal_bar, 16);
-        clc_try_cancel(&steal_answer, &steal_bar);
+      if (lead) {
+        tc_commit(&drain_bar[warp - 9]);
+        mbar_wait_drain(&drain_bar[warp - 9], 0);
       }
       __syncwarp();
-      if (!warp_wait(&steal_bar, n & 1, w)) {
-        mbar_wait_drain(&steal_bar, n & 1);
+    } else if (warp == 11) {
+      // -------------------------------------------------------------- items
+      // The CTA's own item, then those of CTAs that have not started: items
+      // differ in length (documents, causal rows), and this evens them out
+      // without a counter in memory.
+      int idx = static_cast<int>(blockIdx.x);
+      for (uint32_t n = 0;; ++n) {
+        Item it;
+        it.n = -1;
+        if (idx >= 0) it = load_item(p, idx, lane);
+        if (lane == 0) item_sh[n & 1] = it;
         __syncwarp();
-        break;
+        if (lane == 0) mbar_arrive(&item_full);
+        if (idx < 0) break;
+        // not before every warp has taken this one
+        if (!warp_wait(&item_empty, n & 1, w)) break;
+        if (lane == 0) {
+          fence_proxy_async_smem();
+          mbar_expect_tx(&steal_bar, 16);
+          clc_try_cancel(&steal_answer, &steal_bar);
+        }
+        __syncwarp();
+        if (!warp_wait(&steal_bar, n & 1, w)) {
+          mbar_wait_drain(&steal_bar, n & 1);
+          __syncwarp();
+          break;
+        }
+        idx = clc_cancelled(&steal_answer);
       }
-      idx = clc_cancelled(&steal_answer);
+      __syncwarp();
     }
-    __syncwarp();
-  }
   } else {
     regs_raise<kRegsSoftmax>();
     // ------------------------------------------------------------ softmax
@@ -760,25 +762,31 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     bool ok = true;
     uint32_t items = 0, cnt = 0, kv = 0;  // items taken, this tile's key tiles so far, the CTA's
     while (ok) {
-      ok = warp_wait(&item_full, items++ & 1, w);
+      ok = warp_wait(&item_full, items & 1, w);
       if (!ok) break;
-      const Item it = item_sh;
-      if (it.n < 0) break;
+      const Item& it = item_sh[items++ & 1];  // what the key loop does not need stays there
+      const int n_tiles = it.n, lo_all = it.lo;
+      if (n_tiles < 0) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(&item_empty);
-      const int i = it.q0 + 128 * g + r;
-      const bool row = i < a.Nq;
-      RowKeys rk;
-      rk.lo = rk.hi = rk.pos = 0;
-      rk.written = false;
-      if (row) rk = row_keys(a, it.b, i);
+      // A row that is not written reads everything: it must not make tiles look
+      // cut (1000 queries took 17 % longer than 1024 when it did).
+      int klo = -(1 << 30), khi = 0x7fffffff, kpos;
+      bool written;
+      {
+        const int i = it.q0 + 128 * g + r;
+        const RowKeys k = row_keys(a, it.b, min(i, a.Nq - 1));
+        kpos = k.pos;
+        written = k.written && i < a.Nq;
+        if (written) klo = k.lo, khi = k.hi;
+      }
       const float slope2 = (MODE & kBias) && a.slopes ? __ldg(a.slopes + it.h) * kLog2e : 0.f;
       const int first = it.first[g], last = it.last[g];
       float m_run = -INFINITY, l_run = 0.f;
       float s[128];  // the key tile's scores of this row
       for (int j = first; j < last; ++j, ++cnt) {
-        const int base = it.lo + 128 * j;
-        const int rlo = rk.lo - base, rhi = rk.hi - base;
+        const int base = lo_all + 128 * j;
+        const int rlo = klo - base, rhi = khi - base;
         const bool cut = !__all_sync(0xffffffffu, rlo <= 0 && rhi >= 128);
         if (!warp_wait(&s_full[g], cnt & 1, w)) {
           ok = false;
@@ -808,9 +816,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if constexpr ((MODE & kCap) != 0) {
           const bool poly = __all_sync(0xffffffffu, cap.fits(row_max<0, 128, true>(s, 0.f)));
           raw = MODE == kCap && poly && !cut;
-          if (!raw) finish_scores<MODE, BF>(s, cap, poly, c, slope2, static_cast<float>(static_cast<long long>(rk.pos) - base));
+          if (!raw) finish_scores<MODE, BF>(s, cap, poly, c, slope2, static_cast<float>(static_cast<long long>(kpos) - base));
         } else if constexpr (MODE == kBias) {
-          finish_scores<MODE, BF>(s, cap, false, c, slope2, static_cast<float>(static_cast<long long>(rk.pos) - base));
+          finish_scores<MODE, BF>(s, cap, false, c, slope2, static_cast<float>(static_cast<long long>(kpos) - base));
         }
         if (cut) {
 #pragma unroll
@@ -869,7 +877,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           l_run += exp_tile<MODE == 0 ? FROM_DOT : FROM_SCORE, kPolyPairs<MODE>, BF>(s, c2, nm2, cap, tP);
         }
         tmem_wait_st();
-        if (j == it.n - 1 && it.hi - base < 128 && it.hi < a.Nk) {
+        if (j == n_tiles - 1 && it.hi - base < 128 && it.hi < a.Nk) {
           // values behind the last key that any row reads: zeros, since P's
           // zeros would not hide a NaN or an infinity there
           const uint32_t t = kv + static_cast<uint32_t>(j);
@@ -887,7 +895,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[g]);
       }
-      kv += static_cast<uint32_t>(it.n);
+      kv += static_cast<uint32_t>(n_tiles);
       if (!ok) break;
       const bool some = last > first;
       if (some && !warp_wait(&pv_done[g], (cnt - 1) & 1, w)) {
@@ -895,7 +903,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         break;
       }
       tc_fence_after();
-      const bool full_row = rk.hi > rk.lo;
+      const int i = it.q0 + 128 * g + r;
+      const bool row = i < a.Nq, full_row = written && khi > klo;
       const float inv = full_row ? 1.0f / l_run : 0.f;
       // The rows go out through shared memory and TMA, 64 dims at a time: a
       // store instruction over 32 rows of their own took 32 passes, 2000 to
@@ -903,7 +912,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // each thread stores its own.
       uint16_t* dst = a.out + it.b * a.o_b + static_cast<long long>(i) * a.o_n + it.h * a.o_h;
       uint8_t* stage = sm + C::kOffOut + warp * kOutBytes;
-      const bool by_tma = __all_sync(0xffffffffu, !row || rk.written);
+      const bool by_tma = __all_sync(0xffffffffu, !row || written);
       const int row0 = it.q0 + 128 * g + quad * 32;  // the warp's first row
       float odd = 0.f;  // 0 unless a value of the row is not finite
 #pragma unroll 1
@@ -927,7 +936,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (by_tma)
               st_shared_v4(smem_u32(stage) + sw128_offset(lane, (t & 32) + 8 * u), h[4 * u], h[4 * u + 1], h[4 * u + 2],
                            h[4 * u + 3]);
-            else if (row && rk.written && t + 8 * u < a.d)
+            else if (written && t + 8 * u < a.d)
               *reinterpret_cast<uint4*>(dst + t + 8 * u) = make_uint4(h[4 * u], h[4 * u + 1], h[4 * u + 2], h[4 * u + 3]);
           }
         }
@@ -945,7 +954,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // -inf has nothing but the polynomial's 2^-126: such rows anew, by the
       // definition.
       unsigned again =
-          __ballot_sync(0xffffffffu, row && rk.written && full_row && (!(odd == 0.f) || m_run == -INFINITY));
+          __ballot_sync(0xffffffffu, full_row && (!(odd == 0.f) || m_run == -INFINITY));
       if (again) {  // (not before the rows written above have landed)
         if (lane == 0) bulk_wait0();
         __syncwarp();
@@ -954,9 +963,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int src = __ffs(again) - 1;
         again &= again - 1;
         RowKeys o;
-        o.lo = __shfl_sync(0xffffffffu, rk.lo, src);
-        o.hi = __shfl_sync(0xffffffffu, rk.hi, src);
-        o.pos = __shfl_sync(0xffffffffu, rk.pos, src);
+        o.lo = __shfl_sync(0xffffffffu, klo, src);
+        o.hi = __shfl_sync(0xffffffffu, khi, src);
+        o.pos = __shfl_sync(0xffffffffu, kpos, src);
         o.written = true;
         attend_row<BF>(a, it.b, it.q0 + 128 * g + quad * 32 + src, it.h, o, lane);
       }
