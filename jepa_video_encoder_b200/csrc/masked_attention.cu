@@ -432,6 +432,11 @@ __device__ __forceinline__ float exp_tile(const float (&s)[128], uint64_t c2, ui
   return sa + sb;
 }
 
+// The lowest n of 32 bits, n outside 0 .. 32 taken as the nearer end.
+__device__ __forceinline__ uint32_t key_bits(int n) {
+  return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
+
 // mbar_wait whose thread sleeps; a bound of 0 gives up at once as there.
 constexpr uint32_t kSleepNs = 20000;
 __device__ __forceinline__ bool sleep_wait(uint64_t* bar, uint32_t parity, const WaitCtl& w) {
@@ -821,8 +826,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           finish_scores<MODE, BF>(s, cap, false, c, slope2, static_cast<float>(static_cast<long long>(kpos) - base));
         }
         if (cut) {
+          // the allowed keys as bits, 32 at a time: one select a key, its bit
+          // turned into a predicate for several keys at once
 #pragma unroll
-          for (int e = 0; e < 128; ++e) s[e] = (e >= rlo && e < rhi) ? s[e] : -INFINITY;
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t keep = key_bits(rhi - 32 * q) & ~key_bits(rlo - 32 * q);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[32 * q + e] = ((keep >> e) & 1u) ? s[32 * q + e] : -INFINITY;
+          }
         }
         top = early ? row_max<64, 128>(s, top) : row_max<0, 128>(s, top);
         if (MODE == 0) top *= c;
