@@ -142,19 +142,32 @@ __global__ void __launch_bounds__(128) masked_rows_kernel(const MaskedAttnParams
 
 // ------------------------------------------------------------ tensor cores --
 // 128-query tiles on tcgen05.  A work item is 256 query rows (two tiles) of
-// one head; one persistent CTA an SM walks items with a fixed stride.
+// one head.  One CTA an SM (registers, TMEM and shared memory are its own);
+// the grid has a CTA for every item, and a running CTA takes over items of
+// CTAs that have not started, so that items of unequal length even out.
 //   warps 0-3, 4-7  softmax of tile 0 and of tile 1, one thread a row: the
 //                   row's 128 scores of a key tile come from TMEM into
 //                   registers at once, so maxima and sums need no exchange;
 //   warp 8          TMA: Q tiles, then K and V tiles of 128 keys (V as it
 //                   lies, keys by dims: the MN-major B operand of P V);
-//   warps 9, 10     MMA, one issuer a tile: S = Q K^T and O += P V, P from
-//                   TMEM.
+//   warps 9, 10     MMA: S = Q K^T and O += P V, P from TMEM;
+//   warp 11         the items.
 // Heads up to 64 dims: S, P and O of both tiles lie side by side in TMEM and
 // S of the next key tile is computed during the softmax of this one.  Heads
 // up to 128: P takes the place of S, whose product is issued behind P V.
 // O is rescaled only when a row's maximum grew by more than 2^8 (P stays <=
-// 256, the division by the row sum makes it exact again).
+// 256, the division by the row sum makes it exact again).  P is rounded to
+// the 16-bit type for its product; the row sum is of the unrounded values.
+//
+// What bounds it: heads of 128, the tensor cores (9472 keys, 8 heads, bf16:
+// 287 us, 1280 TFLOP/s, beside 1378 for a matrix product sustained under the
+// power limit); heads of 64, the softmax (247 us, 745 TFLOP/s): a pair of
+// key tiles takes 2900 clocks, in which the special-function unit is busy for
+// half, the issue slots for half and the tensor cores for a third, and the
+// rest is the two softmax warps of a scheduler waiting on the same things.
+// Sixteen softmax warps with two or four threads a row fit only with spilled
+// registers, or read the scores twice, and gained nothing (251 to 292 us);
+// the next tile's scores loaded early, with the exponentials (255 to 278 us).
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
