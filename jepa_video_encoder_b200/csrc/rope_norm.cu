@@ -8,8 +8,8 @@
 // turn, its product with the integer position modulo 2^64 is the phase, and
 // the upper 32 bits of that, as a signed number of half-turns in [-1, 1),
 // go to sincospif.
-#include "internal.h"
 #include "head_ops.h"
+#include "internal.h"
 
 namespace jb {
 
@@ -127,9 +127,14 @@ struct alignas(sizeof(T) * VEC) Chunk {
 };
 
 constexpr int kWideThreads = 128;
+// Blocks an SM is to hold at least (0: no bound).  The norms of 16-bit heads
+// would else take 156 registers (12548 x 32 heads of 64: 31 us, with four
+// blocks 28); the other instances lose 5 to 20 % by a bound.
+template <int VEC, int R, int NORM>
+constexpr int kWideBlocks = NORM != NORM_NONE && VEC == 8 && R == 4 ? 4 : 0;
 
 template <typename T, int VEC, int R, int NORM, bool SPLIT>
-__global__ void __launch_bounds__(kWideThreads) head_wide_kernel(const __grid_constant__ WideParams wp) {
+__global__ void __launch_bounds__(kWideThreads, kWideBlocks<VEC, R, NORM>) head_wide_kernel(const __grid_constant__ WideParams wp) {
   using C = Chunk<T, VEC>;
   extern __shared__ float2 cs[];  // [tokens_per][pairs]
   const HeadOpParams& p = wp.op;

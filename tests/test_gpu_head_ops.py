@@ -408,6 +408,17 @@ def test_attention_lengths(Nq, Nk, causal, dtype, d, hq, hk):
         assert not got[:, :Nq - Nk].any()
 
 
+@pytest.mark.parametrize("Nq", [1, 40])
+def test_attention_without_keys(Nq):
+    need_cuda()
+    q = _randn(15, 2, Nq, 4, 64)
+    none = torch.empty(2, 0, 2, 64, dtype=torch.float16, device="cuda")
+    out = torch.full_like(q, 3.0)
+    assert jb.masked_attention(q, none, none, out=out) is out and not out.any()
+    assert not jb.masked_attention(q, none, none, causal=True, cap=5.0).any()
+    _ok()
+
+
 @pytest.mark.parametrize("d", [8, 16, 24, 32, 40, 72, 80, 96, 104, 120])
 @pytest.mark.parametrize("Nq,Nk", [(150, 150), (1, 300)])
 def test_attention_head_dims(d, Nq, Nk):
