@@ -126,6 +126,8 @@ __device__ void attend_row(const MaskedAttnParams& p, int b, int i, int h, const
 
 }  // namespace
 
+// One warp a row.  For more than a few queries over no keys, or over keys that
+// no tensor map describes (one key broadcast along the token axis).
 template <bool BF>
 __global__ void __launch_bounds__(128) masked_rows_kernel(const MaskedAttnParams p) {
   pdl_wait();
@@ -359,9 +361,6 @@ __device__ __forceinline__ void finish_scores(float (&s)[128], const CapPoly<BF>
         s[e] = (MODE & kCap) ? s[e] + bias : fmaf(s[e], c, bias);
       }
     }
-  } else if constexpr (MODE == 0) {
-#pragma unroll
-    for (int e = 0; e < 128; ++e) s[e] *= c;
   }
 }
 
@@ -1545,11 +1544,18 @@ int masked_attention_take_error(unsigned* code) {
   return JEPA_B200_OK;
 }
 
-// Query positions up to which the rows go to the few-query kernel.
-constexpr int kStepQueries = 16;
+// Which kernel: the few-query one up to 32 query positions, and up to 64 where
+// the tiles would leave three quarters of the SMs without an item.  Few-query
+// kernel against tiles, us, at 16, 32 and 64 positions: 2 clips, 4096 keys, 32
+// heads on 8 of 128: 37, 55, 99 against 59; 16 clips, 512 keys, 16 heads of 64:
+// 10, 19, 36 against 21; 64 clips, 300 keys, 12 heads of 64: 24, 45, 85 against
+// 46 to 49; one clip, 16384 keys, 16 heads of 64: 29, 31, 49 against 151.
+static bool few_queries(const MaskedAttnParams& p) {
+  return p.Nq <= 32 || (p.Nq <= 64 && 4ll * p.B * p.hq <= num_sms());
+}
 
 int launch_masked_attention(const MaskedAttnParams& p, bool bf16, cudaStream_t st) {
-  if (p.Nq <= kStepQueries) {
+  if (few_queries(p)) {
     if (p.d <= 64) return bf16 ? launch_step_rows<1, true>(p, st) : launch_step_rows<1, false>(p, st);
     return bf16 ? launch_step_rows<2, true>(p, st) : launch_step_rows<2, false>(p, st);
   } else {
