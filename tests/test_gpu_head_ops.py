@@ -508,6 +508,20 @@ def test_attention_documents(causal, prefix, dtype, d):
     assert kept is out and (out[~written] == 3.0).all() and torch.equal(out[written], got[written])
 
 
+@pytest.mark.parametrize("N", [1, 7, 31, 33, 60])
+@pytest.mark.parametrize("dtype,d", [(torch.float16, 64), (torch.bfloat16, 128)])
+def test_attention_documents_of_few_tokens(N, dtype, d):
+    """Packed rows short enough for the few-query kernel, with rows outside
+    every document."""
+    need_cuda()
+    q, k, v = _qkv(16, 2, N, N, 4, 2, d, dtype)
+    docs = [[0, N // 3, N // 3, N - N // 4], [N // 5, N // 2, N // 2, N]]
+    for mask in (dict(docs=docs), dict(docs=docs, causal=True), dict(docs=docs, causal=True, prefix=[[2, 0, 3], [1, 0, 99]])):
+        out = torch.full_like(q, 3.0)
+        _, written = check_attention(q, k, v, mask=mask, cap=9.0, out=out)
+        assert (out[~written] == 3.0).all()
+
+
 def test_attention_many_short_documents():
     need_cuda()
     rng = np.random.default_rng(1)
