@@ -594,6 +594,12 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+// products below the normal range: zero
+__device__ __forceinline__ uint64_t f2_mul_ftz(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 
 // GELU in its erf form, x * Phi(x), Phi the standard normal CDF: the
 // activation between ffn_up and ffn_down ("Quantization" page, "The rule";
