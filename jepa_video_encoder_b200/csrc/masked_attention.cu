@@ -875,10 +875,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const bool grow = m_new > m_run + kRescale;
         const bool any_grow = __any_sync(0xffffffffu, grow);
         float alpha = 1.0f;
-        if (any_grow && grow) {
-          alpha = ex2_approx(m_run - m_new);  // exp2(-inf) = 0 on the first tile
-          l_run *= alpha;
-          m_run = m_new;
+        if (any_grow) {
+          if (grow) {
+            alpha = ex2_approx(m_run - m_new);  // exp2(-inf) = 0 on the first tile
+            l_run *= alpha;
+            m_run = m_new;
+          }
+          __syncwarp();  // (the TMEM instructions behind want the lanes together)
         }
         // a row that has seen no allowed key yet keeps m = -inf: all its p are 0
         const float m_use = m_run == -INFINITY ? 0.0f : m_run;
@@ -955,6 +958,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll 1
         for (int t = 64 * blk; t < min(a.d, 64 * blk + 64); t += 32) {
           uint32_t o[32];
+          __syncwarp();
           if (some) tmem_ld32(tO + t, o);
           uint32_t h[16];
 #pragma unroll
@@ -1004,6 +1008,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       tc_fence_before();
     }
+    __syncwarp();
     tmem_wait_ld();  // nothing in flight when the columns are given back
     if (lane == 0) bulk_wait0();
   }
@@ -1326,6 +1331,7 @@ __global__ void __launch_bounds__(WARPS * 32, kStepResident<NB, NR, WARPS>) mask
               }
           }
         }
+      __syncwarp();  // (the matrix instructions behind want the lanes together)
     }
     uint32_t pf[NR][kH][2];
 #pragma unroll

@@ -4,6 +4,7 @@ of the C entry points (invalid arguments are rejected before any device
 work, so no GPU is needed)."""
 import ctypes
 import math
+import pathlib
 import subprocess
 
 import pytest
@@ -267,3 +268,16 @@ def test_qk_norm_rope_entry_refuses(lib, kw, status):
     for n, v in kw.items():
         setattr(a, n, v)
     assert lib.jepa_b200_op_qk_norm_rope(ctypes.byref(a), None) == status
+
+
+# ------------------------------------------------------------ kernel sources
+def test_cluster_barriers_are_met_by_whole_warps():
+    """The aligned cluster barrier stands in one function alone, behind a
+    barrier of the warp: lanes reach it from loops of unequal length."""
+    csrc = pathlib.Path(build.CSRC)
+    found = {p.name: p.read_text().count("barrier.cluster") for p in sorted(csrc.iterdir()) if p.suffix in (".cu", ".cuh")}
+    assert {n: c for n, c in found.items() if c} == {"common.cuh": 2}
+    body = (csrc / "common.cuh").read_text()
+    body = body[body.index("void cluster_sync()"):]
+    body = body[:body.index("}")]
+    assert -1 < body.find("__syncwarp();") < body.find("barrier.cluster.arrive")
