@@ -288,26 +288,54 @@ struct TanhPoly<false> {
 // product by its polynomial, s * Q(s^2) - m.
 enum { FROM_DOT = 0, FROM_SCORE = 1, FROM_CAP = 2 };
 
-// Coefficients of cap * log2 e * tanh(s scale / cap) = s Q(s^2) as a
-// polynomial in s^2, and whether it serves: every |s scale / cap| at most 1,
-// no coefficient out of f32's range.
+// cap * log2 e * tanh(z) of a raw dot product s, z = s scale / cap, in two forms:
+// s scale log2 e P(z^2) for |z| <= 1, cap * log2 e * (1 - 2 / (1 + e^2z)) beyond.
+// The second alone would lose a small score in the cap's rounding, cap * 2^-23:
+// at a cap of 1e6 a score of 1 came out as 0.95.
+struct CapScore {
+  float zs, c, kl;  // scale / cap, scale * log2 e, cap * log2 e
+  __device__ __forceinline__ void init(float scale, float cap) {
+    zs = scale / cap;
+    c = scale * kLog2e;
+    kl = cap * kLog2e;
+  }
+  __device__ __forceinline__ float operator()(float s) const {
+    const float z = s * zs, t = z * z;
+    float y = TanhPoly<false>::c(TanhPoly<false>::kTerms - 1);
+#pragma unroll
+    for (int k = TanhPoly<false>::kTerms - 2; k >= 0; --k) y = fmaf(y, t, TanhPoly<false>::c(k));
+    const float far = fmaf(-2.0f * kl, rcp_approx(1.0f + ex2_approx(z * (2.0f * kLog2e))), kl);
+    return fabsf(z) <= 1.0f ? s * c * y : far;
+  }
+};
+
+// Coefficients of the first form as a polynomial s Q(s^2), and the largest |s|
+// that it serves.  That is the one of |z| = 1; where scale / cap is so small
+// that the last coefficients leave f32's normal range they are dropped, and it
+// is the z whose first dropped term is 2^-21 of the score (0.0012 for the linear
+// term alone, caps of 1e17 and more).  None (-1) where they would be infinite.
 template <bool BF>
 struct CapPoly {
   uint64_t q[TanhPoly<BF>::kTerms];
-  float zs, kl;  // scale / cap, cap * log2 e
-  bool usable;
+  float most;
   __device__ __forceinline__ void init(float scale, float cap) {
-    zs = scale / cap;
-    kl = cap * kLog2e;
-    usable = fabsf(zs) > 2e-4f && fabsf(zs) < 1e3f && kl < 1e6f;
-    float f = kl * zs;
+    constexpr float kDropped[5] = {0.0012f, 0.043f, 0.14f, 0.26f, 0.37f};
+    const float zs = scale / cap;
+    float f = scale * kLog2e, z = 1.0f;
+    bool overflow = !(fabsf(f) < 1e36f);
 #pragma unroll
     for (int k = 0; k < TanhPoly<BF>::kTerms; ++k) {
-      q[k] = f2_pack(TanhPoly<BF>::c(k) * f, TanhPoly<BF>::c(k) * f);
-      f *= zs * zs;
+      if (k > 0) {
+        f *= zs * zs;
+        if (z == 1.0f && !(fabsf(f) > 1e-35f)) z = kDropped[k - 1];
+      }
+      const float v = z < 1.0f ? 0.0f : TanhPoly<BF>::c(k) * f;
+      q[k] = f2_pack(v, v);
     }
+    overflow |= !(fabsf(f) < 1e36f);
+    most = overflow ? -1.0f : z / fabsf(zs);
   }
-  __device__ __forceinline__ bool fits(float big) const { return usable && big * fabsf(zs) <= 1.0f; }
+  __device__ __forceinline__ bool fits(float big) const { return big <= most; }
   // Q(s^2) of two scores
   __device__ __forceinline__ uint64_t slope(uint64_t s) const {
     const uint64_t t = f2_mul(s, s);
@@ -316,16 +344,12 @@ struct CapPoly {
     for (int k = TanhPoly<BF>::kTerms - 2; k >= 0; --k) y = f2_fma(y, t, q[k]);
     return y;
   }
-  // any score: kl (1 - 2 / (1 + e^2z))
-  __device__ __forceinline__ float exact(float s) const {
-    return fmaf(-2.0f * kl, rcp_approx(1.0f + ex2_approx(s * (2.0f * kLog2e * zs))), kl);
-  }
 };
 
 // Raw dot products in s[] to scores in the exp2 domain.
 template <int MODE, bool BF>
-__device__ __forceinline__ void finish_scores(float (&s)[128], const CapPoly<BF>& cap, bool poly, float c, float slope2,
-                                              float dist0) {
+__device__ __forceinline__ void finish_scores(float (&s)[128], const MaskedAttnParams& a, const CapPoly<BF>& cap, bool poly,
+                                              float c, float slope2, float dist0) {
   if constexpr ((MODE & kCap) != 0) {
     if (poly) {
 #pragma unroll
@@ -334,8 +358,10 @@ __device__ __forceinline__ void finish_scores(float (&s)[128], const CapPoly<BF>
         f2_unpack(f2_mul(v, cap.slope(v)), s[e], s[e + 1]);
       }
     } else {
+      CapScore any;
+      any.init(a.scale, a.cap);
 #pragma unroll
-      for (int e = 0; e < 128; ++e) s[e] = cap.exact(s[e]);
+      for (int e = 0; e < 128; ++e) s[e] = any(s[e]);
     }
   }
   if constexpr ((MODE & kBias) != 0) {
@@ -840,12 +866,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (lane == 0) mbar_arrive(&s_free[g]);
         }
         bool raw = MODE == 0;  // exponents straight from the dot products
+        [[maybe_unused]] const float dist0 = static_cast<float>(static_cast<long long>(kpos) - base);
         if constexpr ((MODE & kCap) != 0) {
           const bool poly = __all_sync(0xffffffffu, cap.fits(row_max<0, 128, true>(s, 0.f)));
           raw = MODE == kCap && poly && !cut;
-          if (!raw) finish_scores<MODE, BF>(s, cap, poly, c, slope2, static_cast<float>(static_cast<long long>(kpos) - base));
+          if (!raw) finish_scores<MODE, BF>(s, a, cap, poly, c, slope2, dist0);
         } else if constexpr (MODE == kBias) {
-          finish_scores<MODE, BF>(s, cap, false, c, slope2, static_cast<float>(static_cast<long long>(kpos) - base));
+          finish_scores<MODE, BF>(s, a, cap, false, c, slope2, dist0);
         }
         if (cut) {
           // the allowed keys as bits, 32 at a time: one select a key, its bit
@@ -1241,7 +1268,8 @@ __global__ void __launch_bounds__(WARPS * 32, kStepResident<NB, NR, WARPS>) mask
       for (int t = 0; t < 4; ++t) o[x][n][t][0] = o[x][n][t][1] = o[x][n][t][2] = o[x][n][t][3] = 0.f;
   }
   const float c = a.scale * kLog2e;
-  const float zs2 = a.cap > 0.f ? 2.0f * kLog2e * a.scale / a.cap : 0.f, kl = a.cap * kLog2e;
+  CapPoly<BF> cap;
+  if (a.cap > 0.f) cap.init(a.scale, a.cap);
   if (warp < tiles) {
     load_k(k0 + warp * kKeys);
     load_v(k0 + warp * kKeys);
@@ -1265,10 +1293,24 @@ __global__ void __launch_bounds__(WARPS * 32, kStepResident<NB, NR, WARPS>) mask
       }
     if (more) load_k(key0 + WARPS * kKeys);
     if (a.cap > 0.f) {
+      float big = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4 * kH * NR; ++i) {
-        float& v = s[i / (4 * kH)][(i >> 2) % kH][i & 3];
-        v = fmaf(-2.0f * kl, rcp_approx(1.0f + ex2_approx(v * zs2)), kl);
+      for (int i = 0; i < 4 * kH * NR; ++i) big = fmaxf(big, fabsf(s[i / (4 * kH)][(i >> 2) % kH][i & 3]));
+      if (__all_sync(0xffffffffu, cap.fits(big))) {
+#pragma unroll
+        for (int i = 0; i < 4 * kH * NR; i += 2) {
+          float(&v)[4] = s[i / (4 * kH)][(i >> 2) % kH];
+          const uint64_t d = f2_pack(v[i & 3], v[(i & 3) + 1]);
+          f2_unpack(f2_mul(d, cap.slope(d)), v[i & 3], v[(i & 3) + 1]);
+        }
+      } else {
+        CapScore any;
+        any.init(a.scale, a.cap);
+#pragma unroll
+        for (int i = 0; i < 4 * kH * NR; ++i) {
+          float& v = s[i / (4 * kH)][(i >> 2) % kH][i & 3];
+          v = any(v);
+        }
       }
     } else {
 #pragma unroll
