@@ -138,16 +138,16 @@ int jepa_b200_op_sync_status(void* stream) {
   DevErr* e = op_err();
   if (!e) return JEPA_B200_ERR_CUDA;
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return JEPA_B200_ERR_CUDA;
+  // both words are read and cleared before either decides: the calls before
+  // this one leave nothing for the next
   DevErr h{0, 0};
   if (cudaMemcpy(&h, e, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess) return JEPA_B200_ERR_CUDA;
-  if (h.code != DERR_NONE) {
-    cudaMemset(e, 0, sizeof(DevErr));
-    return h.code == DERR_TIMEOUT ? JEPA_B200_ERR_TIMEOUT : JEPA_B200_ERR_CUDA;
-  }
-  unsigned code = 0;
-  if (masked_attention_take_error(&code) != JEPA_B200_OK) return JEPA_B200_ERR_CUDA;
-  if (code != DERR_NONE) return code == DERR_TIMEOUT ? JEPA_B200_ERR_TIMEOUT : JEPA_B200_ERR_CUDA;
-  return JEPA_B200_OK;
+  if (h.code != DERR_NONE) cudaMemset(e, 0, sizeof(DevErr));
+  unsigned masked = 0;
+  if (masked_attention_take_error(&masked) != JEPA_B200_OK) return JEPA_B200_ERR_CUDA;
+  for (const unsigned code : {h.code, masked})
+    if (code != DERR_NONE && code != DERR_TIMEOUT) return JEPA_B200_ERR_CUDA;
+  return h.code == DERR_NONE && masked == DERR_NONE ? JEPA_B200_OK : JEPA_B200_ERR_TIMEOUT;
 }
 
 int jepa_b200_op_layernorm(const float* x, int rows, int D, int in_row_stride, const float* gamma,
