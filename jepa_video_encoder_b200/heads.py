@@ -155,15 +155,36 @@ def _new(like, shape, stream, zero: bool = False):
 class RopePlan:
     """Frequencies of a rotation (rope_plan makes it; a program keeps it; it
     serves every device).  Pairs of dims turn by position * inv_freq
-    radians."""
+    radians.  The arrays that go to the library are made from these numbers
+    here, in every copy and unpickled plan anew, so that a plan passes the
+    addresses of its own arrays."""
     rot_dim: int
     layout: str
     sections: Tuple[int, ...]
     inv_freq: Tuple[float, ...]   # radians per unit of position, one a pair
     factor: float                 # on cosine and sine
-    turns: Any = field(repr=False)   # uint64 [pairs]: inv_freq / 2 pi as binary fractions
-    axis: Any = field(repr=False)    # uint8 [pairs]
-    addresses: Tuple[int, int] = field(repr=False)   # of turns and axis
+    turns: Any = field(init=False, repr=False, compare=False)   # uint64 [pairs]: inv_freq / 2 pi as binary fractions
+    axis: Any = field(init=False, repr=False, compare=False)    # uint8 [pairs]
+    addresses: Tuple[int, int] = field(init=False, repr=False, compare=False)   # of turns and axis
+
+    def __post_init__(self):
+        if self.layout not in _LAYOUTS:
+            raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {self.layout!r}")
+        if not 2 <= self.rot_dim <= 256 or self.rot_dim % 2:
+            raise ValueError(f"rot_dim must be even, at least 2 and at most 256, got {self.rot_dim}")
+        if not 1 <= len(self.sections) <= 3 or min(self.sections) < 1 or sum(self.sections) != self.rot_dim // 2:
+            raise ValueError(f"sections must be 1 to 3 positive counts of pairs that add up to {self.rot_dim // 2}, "
+                             f"got {self.sections}")
+        if len(self.inv_freq) != self.rot_dim // 2 or not all(math.isfinite(w) for w in self.inv_freq):
+            raise ValueError(f"inv_freq must be {self.rot_dim // 2} finite numbers")
+        turns = array("Q", rope_turns(self.inv_freq))
+        axis = array("B", [a for a, n in enumerate(self.sections) for _ in range(n)])
+        object.__setattr__(self, "turns", turns)
+        object.__setattr__(self, "axis", axis)
+        object.__setattr__(self, "addresses", (turns.buffer_info()[0], axis.buffer_info()[0]))
+
+    def __reduce__(self):
+        return RopePlan, (self.rot_dim, self.layout, self.sections, self.inv_freq, self.factor)
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, sections: Optional[Sequence[int]] = None,
@@ -239,11 +260,9 @@ def rope_plan(rot_dim: int, *, layout: str = "half", base: float = 10000.0, sect
         raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
     if rot_dim > 256:
         raise ValueError(f"rot_dim must be at most 256, got {rot_dim}")
-    freq, axis, factor = rope_frequencies(rot_dim, base, sections, scaling)
+    freq, _, factor = rope_frequencies(rot_dim, base, sections, scaling)
     sections = (rot_dim // 2,) if sections is None else tuple(int(n) for n in sections)
-    turns, axes = array("Q", rope_turns(freq)), array("B", axis)
-    return RopePlan(rot_dim, layout, sections, freq, factor, turns, axes,
-                    (turns.buffer_info()[0], axes.buffer_info()[0]))
+    return RopePlan(rot_dim, layout, sections, freq, factor)
 
 
 def check_positions(positions, n_axes: int, B: int, N: int) -> Tuple[int, int, int]:

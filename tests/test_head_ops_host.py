@@ -2,9 +2,12 @@
 turn fractions, the argument structures, and every refusal of the binding and
 of the C entry points (invalid arguments are rejected before any device
 work, so no GPU is needed)."""
+import copy
 import ctypes
+import dataclasses
 import math
 import pathlib
+import pickle
 import subprocess
 
 import pytest
@@ -180,6 +183,45 @@ def test_outputs_that_overlap_are_refused():
     with pytest.raises(ValueError, match="share memory"):
         heads.check_output(_cpu(400).as_strided((1, 4, 2, 64), (0, 64, 32, 1)), "out", [])
     heads.check_output(_cpu(2, 2, 4, 64).transpose(1, 2), "out", [])
+
+
+# --------------------------------------------------------- copies of a plan
+def _own_addresses(plan):
+    assert plan.addresses == (plan.turns.buffer_info()[0], plan.axis.buffer_info()[0])
+    assert len(plan.turns) == len(plan.axis) == plan.rot_dim // 2
+
+
+@pytest.mark.parametrize("how", [copy.copy, copy.deepcopy, lambda p: pickle.loads(pickle.dumps(p)), dataclasses.replace])
+def test_a_copied_plan_holds_its_own_numbers(how):
+    """The addresses that go to the library are those of the copy's arrays,
+    not of the original's, which may be gone."""
+    plan = jb.rope_plan(60, layout="interleaved", sections=(10, 10, 10), scaling={"type": "linear", "factor": 4.0})
+    got = how(plan)
+    _own_addresses(plan)
+    _own_addresses(got)
+    assert got == plan and list(got.turns) == list(plan.turns) and list(got.axis) == list(plan.axis)
+    for name in ("rot_dim", "layout", "sections", "inv_freq", "factor"):
+        assert getattr(got, name) == getattr(plan, name)
+
+
+def test_a_module_with_a_plan_is_copied():
+    m = torch.nn.Module()
+    m.plan = jb.rope_plan(64)
+    twin = copy.deepcopy(m)
+    _own_addresses(twin.plan)
+    assert twin.plan.turns is not m.plan.turns
+
+
+def test_a_plan_whose_numbers_are_replaced():
+    """The arrays follow the frequencies; what does not fit is refused."""
+    plan = jb.rope_plan(8)
+    slow = dataclasses.replace(plan, inv_freq=tuple(f / 2 for f in plan.inv_freq), factor=0.5)
+    _own_addresses(slow)
+    assert list(slow.turns) == heads.rope_turns(slow.inv_freq) and slow.factor == 0.5
+    for bad in (dict(inv_freq=plan.inv_freq[:3]), dict(sections=(3,)), dict(sections=(1, 1, 1, 1)), dict(sections=(4, 0)),
+                dict(rot_dim=10), dict(rot_dim=7), dict(rot_dim=258), dict(layout="other"), dict(inv_freq=(1.0, 0.1, 0.01, math.nan))):
+        with pytest.raises(ValueError):
+            dataclasses.replace(plan, **bad)
 
 
 # ------------------------------------------------------- refusals of the ABI
