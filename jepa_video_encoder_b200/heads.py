@@ -8,7 +8,7 @@ views of one projection output or of a cache included.  The calls are
 asynchronous on ``stream`` (default: the current stream), allocate nothing but
 an output that was not given, keep nothing between calls, and can be captured
 into CUDA graphs.  They are forward only: a tensor that requires grad is
-refused while autograd records.
+refused while autograd records, and so is one that carries a tangent.
 """
 from __future__ import annotations
 
@@ -18,6 +18,7 @@ from dataclasses import dataclass, field
 from typing import Any, Optional, Sequence, Tuple
 
 import torch
+import torch.autograd.forward_ad as fwAD
 
 from . import _abi
 from ._abi import check, load_library
@@ -36,14 +37,22 @@ _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: _abi.BF16}
 
 
 # ---------------------------------------------------------------- operands
+def check_forward_only(t, name: str) -> None:
+    """Refuse a tensor that autograd follows in reverse mode (while it
+    records) or in forward mode (a tangent of the current level)."""
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires grad: the per-head operators are forward only (call them under "
+                         "torch.no_grad() or on detached tensors)")
+    if fwAD._current_level >= 0 and fwAD.unpack_dual(t).tangent is not None:
+        raise ValueError(f"{name} has a tangent: the per-head operators do not carry one on (call them on its primal)")
+
+
 def _check_cuda(t, name: str, device: int) -> None:
     if t.get_device() != device:
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
         raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{device}")
-    if t.requires_grad and torch.is_grad_enabled():
-        raise ValueError(f"{name} requires grad: the per-head operators are forward only (call them under "
-                         "torch.no_grad() or on detached tensors)")
+    check_forward_only(t, name)
 
 
 def check_heads(t, name: str, dtype=None, shape: Optional[Sequence[int]] = None, granule: int = 1):
@@ -344,7 +353,7 @@ def _weight(t, name: str, heads: int, d: int, device: int) -> Tuple[int, int]:
     shape, strides = t.shape, t.stride()
     if (shape != (d,) and shape != (heads, d)) or (d > 1 and strides[-1] != 1):
         raise ValueError(f"{name} must be [{d}] or [{heads}, {d}] with a contiguous last axis, got {list(shape)}")
-    if t.get_device() != device or t.requires_grad:
+    if t.get_device() != device or t.requires_grad or fwAD._current_level >= 0:
         _check_cuda(t, name, device)
     return t.data_ptr(), strides[0] if len(shape) == 2 else 0
 

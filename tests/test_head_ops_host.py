@@ -12,6 +12,7 @@ import subprocess
 
 import pytest
 import torch
+import torch.autograd.forward_ad as fwAD
 
 import jepa_video_encoder_b200 as jb
 from jepa_video_encoder_b200 import _abi, build, heads
@@ -183,6 +184,26 @@ def test_outputs_that_overlap_are_refused():
     with pytest.raises(ValueError, match="share memory"):
         heads.check_output(_cpu(400).as_strided((1, 4, 2, 64), (0, 64, 32, 1)), "out", [])
     heads.check_output(_cpu(2, 2, 4, 64).transpose(1, 2), "out", [])
+
+
+# ------------------------------------------------------------- forward only
+def test_tensors_that_autograd_follows_are_refused():
+    """Reverse mode where it records, forward mode within its level; a plain
+    tensor beside a dual one passes."""
+    x = torch.zeros(2, 3)
+    heads.check_forward_only(x, "x")
+    with pytest.raises(ValueError, match="forward only"):
+        heads.check_forward_only(x.clone().requires_grad_(), "x")
+    with torch.no_grad():
+        heads.check_forward_only(x.clone().requires_grad_(), "x")
+    with fwAD.dual_level():
+        dual = fwAD.make_dual(x.clone(), torch.ones(2, 3))
+        heads.check_forward_only(x, "x")
+        with pytest.raises(ValueError, match="tangent"):
+            heads.check_forward_only(dual, "x")
+        with torch.no_grad(), pytest.raises(ValueError, match="tangent"):   # which does not stop forward mode
+            heads.check_forward_only(dual, "x")
+    heads.check_forward_only(x, "x")
 
 
 # --------------------------------------------------------- copies of a plan
