@@ -7,7 +7,12 @@ Operands are CUDA tensors [B, N, heads, head_dim] with a contiguous last axis,
 views of one projection output or of a cache included.  The calls are
 asynchronous on ``stream`` (default: the current stream), allocate nothing but
 an output that was not given, keep nothing between calls, and can be captured
-into CUDA graphs.  They are forward only: a tensor that requires grad is
+into CUDA graphs.  With a ``stream`` that is not the current one the operands
+may be dropped as soon as the call returns: their memory is not given out
+again before the stream has passed it.  Their contents must be ready on it
+(stream.wait_stream), and an output that was not given belongs to it.
+
+The operators are forward only: a tensor that requires grad is
 refused while autograd records, and so is one that carries a tangent.
 """
 from __future__ import annotations
@@ -144,6 +149,15 @@ def _launch(t, stream):
     if stream.device_index != device:
         raise ValueError(f"the stream is on cuda:{stream.device_index}, but the current device is cuda:{device}")
     return device, stream.cuda_stream
+
+
+def _hold(device: int, raw: int, stream, tensors) -> None:
+    """Tell the allocator that a stream other than the current one, whose
+    memory they are, uses these tensors."""
+    if stream is not None and raw != _raw_stream(device):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
 
 
 def _new(like, shape, stream, zero: bool = False):
@@ -337,6 +351,7 @@ def rope(x, positions, plan: RopePlan, out=None, stream=None):
         check_output(out, "out", [(x, "x", True), (positions, "positions", False)])
     if not (B and N and H):
         return out
+    _hold(device, raw, stream, (x, positions, out))
     check(load_library().jepa_b200_op_rope(_ROPE.pack(*at_x, *at_out, dtype, B, N, H, d, *words), raw), "rope")
     return out
 
@@ -414,6 +429,7 @@ def qk_norm_rope(q, k, positions, plan: Optional[RopePlan], q_weight, k_weight, 
         check_output(k_out, "k_out", [(k, "k", True), (q, "q", False), (q_out, "q_out", False)] + others())
     if not (B and N and (hq or hk)):
         return q_out, k_out
+    _hold(device, raw, stream, (q, k, positions, q_weight, k_weight, q_bias, k_bias, q_out, k_out))
     check(load_library().jepa_b200_op_qk_norm_rope(
         _QK.pack(*at_q, *at_k, *at_qo, *at_ko, dtype, B, N, hq, hk, d, _NORMS[norm], eps, qw, qb, kw, kb, qw_h, qb_h,
                  kw_h, kb_h, *words), raw), "qk_norm_rope")
@@ -507,6 +523,7 @@ def masked_attention(q, k, v, *, scale: Optional[float] = None, cap: Optional[fl
                                   (q_start, "q_start", False), (slopes, "slopes", False)])
     if not (B and Nq):
         return out
+    _hold(device, raw, stream, (q, k, v, slopes, prefix, doc_offsets, kv_len, q_start, out))
     check(load_library().jepa_b200_op_masked_attention(
         _ATTN.pack(*at_q, *at_k, *at_v, *at_out, dtype, B, Nq, Nk, hq, hk, d, scale, cap,
                    1 if causal else 0, n_docs, at_slopes, at_prefix, at_docs, at_len, at_start), raw),
