@@ -99,7 +99,7 @@ def check_output(out, name: str, inputs) -> None:
     """Validate an output that the caller gave: no two of its elements in one
     place, and no overlap with ``inputs``, a list of (tensor, name, may be the
     output itself).  Views whose ranges of memory interleave count as
-    overlapping unless their elements can be told apart by their rows."""
+    overlapping unless they lie in separate columns of a common step."""
     axes = sorted((s, n) for n, s in zip(out.shape, out.stride()) if n > 1)
     reach = 1
     for s, n in axes:
@@ -118,25 +118,28 @@ def check_output(out, name: str, inputs) -> None:
         o1, t1 = o0 + _span(out) * out.element_size(), t0 + _span(t) * t.element_size()
         if o1 <= t0 or t1 <= o0:
             continue
-        if not _rows_apart(out, t):
+        if not _columns_apart(out, t):
             raise ValueError(f"{name} overlaps {what}")
 
 
-def _rows_apart(a, b) -> bool:
-    """Whether two [B, N, h, d] views step through memory in the same rows and
-    lie in separate columns of them, as slices of one projection output do."""
-    if a.dim() != 4 or b.dim() != 4 or a.dtype != b.dtype:
+def _columns_apart(a, b) -> bool:
+    """Whether two views lie in separate columns of some common step: a stride
+    of one of them by which every larger stride of both is a whole number of
+    steps, as with slices of one projection output (the step of a token) and
+    with the heads of q, k and v in turn (the step of a head)."""
+    size = a.element_size()
+    if a.dtype != b.dtype or (b.data_ptr() - a.data_ptr()) % size:
         return False
-    axis = 1 if max(a.shape[1], b.shape[1]) > 1 else 0  # one token a clip: the rows are the clips
-    row = a.stride(axis)
-    if min(a.shape[axis], b.shape[axis]) < 2 or row != b.stride(axis) or row < 1:
-        return False
-    off, wide = (b.data_ptr() - a.data_ptr()) // a.element_size() % row, []
-    for x in (a, b):
-        if axis == 1 and x.shape[0] > 1 and x.stride(0) % row:
-            return False
-        wide.append(1 + sum((n - 1) * s for n, s in zip(x.shape[2:], x.stride()[2:])))
-    return wide[0] <= off and off + wide[1] <= row
+    axes = [[(n, s) for n, s in zip(x.shape, x.stride()) if n > 1] for x in (a, b)]
+    for step in {s for x in axes for _, s in x if s > 1}:
+        inside = [[(n, s) for n, s in x if s % step] for x in axes]
+        if any(s > step for x in inside for _, s in x):
+            continue
+        wide = [1 + sum((n - 1) * s for n, s in x) for x in inside]
+        off = (b.data_ptr() - a.data_ptr()) // size % step
+        if wide[0] <= off and off + wide[1] <= step:
+            return True
+    return False
 
 
 def _launch(t, stream):

@@ -8,6 +8,7 @@ import dataclasses
 import math
 import pathlib
 import pickle
+import random
 import subprocess
 
 import pytest
@@ -184,6 +185,47 @@ def test_outputs_that_overlap_are_refused():
     with pytest.raises(ValueError, match="share memory"):
         heads.check_output(_cpu(400).as_strided((1, 4, 2, 64), (0, 64, 32, 1)), "out", [])
     heads.check_output(_cpu(2, 2, 4, 64).transpose(1, 2), "out", [])
+
+
+def test_views_that_interleave_are_told_apart():
+    """Columns of any common step: heads of q, k and v in turn, with and
+    without more tokens and clips; views that do meet are refused."""
+    for B, N in ((2, 4), (1, 4), (2, 1), (1, 1)):
+        x = _cpu(B, N, 3, 3, 64)          # [heads, q / k / v, head_dim]
+        q, k, v = x.unbind(3)
+        heads.check_output(q, "q_out", [(q, "q", True), (k, "k", False), (v, "v", False)])
+        heads.check_output(v, "out", [(q, "q", False), (k, "k", False)])
+        heads.check_output(x[..., 1, 32:], "out", [(x[..., 1, :32], "x", False)])    # halves of a head
+        for a, b in ((x[..., 0, :], x[..., 0, :32]), (x[..., 0, 16:48], x[..., 0, :32])):
+            with pytest.raises(ValueError, match="overlaps"):
+                heads.check_output(a, "out", [(b, "x", False)])
+    x = _cpu(2, 4, 6, 64)
+    with pytest.raises(ValueError, match="overlaps"):
+        heads.check_output(x[:, :, ::2], "out", [(x[:, :, 2:5], "x", False)])
+    heads.check_output(x[:, :, ::2], "out", [(x[:, :, 1::2], "x", False)])
+    flat = _cpu(4096)
+    a, b = flat.as_strided((1, 4, 2, 8), (0, 24, 8, 1)), flat.as_strided((1, 4, 2, 8), (0, 32, 8, 1), 16)
+    with pytest.raises(ValueError, match="overlaps"):     # other steps: b's second row lies in a's third
+        heads.check_output(a, "out", [(b, "x", False)])
+
+
+def test_apart_means_no_element_in_common():
+    """The rule against the elements themselves, for strided views at random:
+    never apart where one is shared."""
+    rng, told = random.Random(3), 0
+    flat = _cpu(1 << 14)
+    for _ in range(3000):
+        views = []
+        row = rng.choice([8, 12, 24, 48])
+        for _ in range(2):
+            shape = [rng.choice([1, 2, 3]) for _ in range(3)] + [rng.choice([1, 4, 8])]
+            strides = [rng.choice([0, row, 2 * row, 96, 5]) for _ in range(3)] + [1]
+            views.append(flat.as_strided(shape, strides, rng.randrange(64)))
+        idx = [set(torch.arange(1 << 14).as_strided(v.shape, v.stride(), v.storage_offset()).flatten().tolist()) for v in views]
+        if heads._columns_apart(*views):
+            told += 1
+            assert not idx[0] & idx[1], [(v.shape, v.stride(), v.storage_offset()) for v in views]
+    assert told > 50
 
 
 # ------------------------------------------------------------- forward only
