@@ -519,7 +519,10 @@ JEPA_B200_API int jepa_b200_op_qk_norm_rope(const jepa_b200_qk_norm_rope_args *a
  *     tokens of it; kv_len and q_start are not read.
  * A row without an allowed key gets zeros.  A row outside every document is
  * not written.  Keys and values that a row may not read never reach it,
- * whatever they hold (NaN, infinities).  kv_len is clamped to 0 .. Nk.
+ * whatever they hold (NaN, infinities).  Rows that come out with a value that
+ * is not finite are computed a second time, one warp a row, at some 5 us for 32
+ * keys and warp: a NaN that many rows read makes a call slow, and its device
+ * waits are not held to their bound meanwhile.  kv_len is clamped to 0 .. Nk.
  * dtype F16 or BF16; head_dim a multiple of 8, 8 .. 128; every data pointer
  * 16-byte aligned and every stride a multiple of 8 elements.  Scores, softmax
  * statistics and sums are f32; the probabilities are rounded to dtype for the

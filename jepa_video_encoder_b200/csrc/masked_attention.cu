@@ -66,9 +66,12 @@ __device__ __forceinline__ float finish_score(const MaskedAttnParams& p, float d
 
 // One query row by one warp, straight from the definition: 32 keys at a
 // time, one per lane, for the scores; then each lane sums its own output
-// dims over the 32 probabilities.  Keys outside [lo, hi) are never read.
+// dims over the 32 probabilities.  Keys outside [lo, hi) are never read.  The
+// time that it takes goes to *spent as it passes, for warps that wait meanwhile.
 template <bool BF>
-__device__ void attend_row(const MaskedAttnParams& p, int b, int i, int h, const RowKeys& r, int lane) {
+__device__ void attend_row(const MaskedAttnParams& p, int b, int i, int h, const RowKeys& r, int lane,
+                           unsigned long long* spent = nullptr) {
+  unsigned long long since = spent ? globaltimer() : 0;
   const int hk = h / (p.hq / p.hk);
   const uint16_t* q = p.q + b * p.q_b + i * p.q_n + h * p.q_h;
   const uint16_t* k = p.k + b * p.k_b + hk * p.k_h;
@@ -78,6 +81,11 @@ __device__ void attend_row(const MaskedAttnParams& p, int b, int i, int h, const
   float m = -INFINITY, l = 0.f;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};  // dims lane, lane + 32, ...
   for (int j0 = r.lo; j0 < r.hi; j0 += 32) {
+    if (spent && lane == 0) {
+      const unsigned long long now = globaltimer();
+      atomicAdd(spent, now - since);
+      since = now;
+    }
     const int j = j0 + lane;
     float s = -INFINITY;
     if (j < r.hi) {
@@ -485,9 +493,14 @@ __device__ __forceinline__ uint32_t key_bits(int n) {
   return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
 }
 
-// mbar_wait whose thread sleeps; a bound of 0 gives up at once as there.
+// mbar_wait whose thread sleeps; a bound of 0 gives up at once as there.  The
+// time that the CTA's warps have spent on rows computed anew (attend_row: up to
+// 32 rows a warp at some 4.7 us for 32 keys) is added to the bound.
+struct TileWait : WaitCtl {
+  volatile unsigned long long* spent;
+};
 constexpr uint32_t kSleepNs = 20000;
-__device__ __forceinline__ bool sleep_wait(uint64_t* bar, uint32_t parity, const WaitCtl& w) {
+__device__ __forceinline__ bool sleep_wait(uint64_t* bar, uint32_t parity, const TileWait& w) {
   if (mbar_try_wait(bar, parity)) return true;
   if (w.timeout_ns == 0) {
     raise_error(w, DERR_TIMEOUT);
@@ -496,7 +509,7 @@ __device__ __forceinline__ bool sleep_wait(uint64_t* bar, uint32_t parity, const
   const unsigned long long t0 = globaltimer();
   while (!mbar_try_wait_for(bar, parity, kSleepNs)) {
     if (*w.abort) return false;
-    if (globaltimer() - t0 > w.timeout_ns) {
+    if (globaltimer() - t0 > w.timeout_ns + *w.spent) {
       raise_error(w, DERR_TIMEOUT);
       return false;
     }
@@ -504,7 +517,7 @@ __device__ __forceinline__ bool sleep_wait(uint64_t* bar, uint32_t parity, const
   return true;
 }
 // The same by a whole warp, its lanes together again behind it.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& w) {
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const TileWait& w) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, sleep_wait(bar, parity, w));
 }
@@ -534,6 +547,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __shared__ Item item_sh[2];
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
+  __shared__ unsigned long long spent_sh;  // ns, in rows computed anew
 
   const uint32_t raw = smem_u32(dsmem);
   uint8_t* sm = dsmem + ((1024u - (raw & 1023u)) & 1023u);
@@ -563,6 +577,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     mbar_init(&item_empty, 1 + (C::kAliasP ? 1 : 2) + 8);  // TMA, MMA and softmax warps
     mbar_init(&steal_bar, 1);
     abort_sh = 0;
+    spent_sh = 0;
     mbar_fence_init();
   }
   if (warp == 9) {
@@ -576,8 +591,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   pdl_wait();
   pdl_trigger();
 
-  WaitCtl w;
+  TileWait w;
   w.abort = reinterpret_cast<volatile int*>(&abort_sh);
+  w.spent = reinterpret_cast<volatile unsigned long long*>(&spent_sh);
   w.err = &g_masked_err;
   w.timeout_ns = a.timeout_ns;
   w.where = (KID_ATTN << 8) | static_cast<unsigned>(warp);
@@ -1016,7 +1032,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // A value that is not finite may have come from a key that the row does
       // not read (0 * inf in the tile's product), and a row whose scores are all
       // -inf may have nothing but the polynomial's 2^-126: such rows anew, by the
-      // definition.
+      // definition.  One warp a row, and slow: an infinity among the values of
+      // 8192 keys that every row reads makes 16 heads of 64 take 153 ms in place
+      // of 0.47 (of one head alone 40).
       unsigned again =
           __ballot_sync(0xffffffffu, full_row && (!(odd == 0.f) || m_run == -INFINITY));
       if (again) {  // (not before the rows written above have landed)
@@ -1031,7 +1049,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         o.hi = __shfl_sync(0xffffffffu, khi, src);
         o.pos = __shfl_sync(0xffffffffu, kpos, src);
         o.written = true;
-        attend_row<BF>(a, it.b, it.q0 + 128 * g + quad * 32 + src, it.h, o, lane);
+        attend_row<BF>(a, it.b, it.q0 + 128 * g + quad * 32 + src, it.h, o, lane, &spent_sh);
       }
       tc_fence_before();
     }

@@ -40,3 +40,26 @@ def test_status_is_cleared_of_every_call_at_once(first):
     assert jb.op_sync_status() == 0
     assert torch.equal(got, want)
     assert ((out.double() - a.double() @ w.double().T).abs() <= 1024 * 2.0 ** -22 * (a.double().abs() @ w.double().abs().T)).all()
+
+
+def test_rows_computed_anew_do_not_run_out_of_time():
+    """A value that is not finite sends the rows that read it through the
+    definition, which takes longer than the wait bound set here; the CTAs that
+    go on to another item wait for theirs meanwhile."""
+    need_cuda()
+    q, k, v = _qkv(9, 1, 2048, 2048, 40, 40, 64, torch.float16)
+    v[0, 7] = float("inf")
+    want = jb.masked_attention(q, k, v)
+    assert jb.op_sync_status() == 0
+    start, end = torch.cuda.Event(True), torch.cuda.Event(True)
+    jb.op_set_timeout_ns(2_000_000)
+    try:
+        start.record()
+        got = jb.masked_attention(q, k, v)
+        end.record()
+        status = jb.op_sync_status()
+    finally:
+        jb.op_set_timeout_ns(4_000_000_000)
+    assert status == 0
+    assert start.elapsed_time(end) > 2
+    assert torch.equal(got, want) and not torch.isfinite(got).any()
