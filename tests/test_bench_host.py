@@ -2,6 +2,8 @@
 roofline divides by, the oracle's timed sample, and the reference arm's line."""
 import json
 import os
+import re
+import subprocess
 import sys
 
 import numpy as np
@@ -90,6 +92,24 @@ def test_source_hash_ignores_comments_not_code():
     assert bench.hash_sources([src.replace("int* p", "long* p")]) != h
     assert bench.hash_sources([src, ""]) != h                                    # file boundaries count
     assert "//" in bench.code_text(src) and "bump" not in bench.code_text(src)  # '//' inside the literal kept
+
+
+def test_traffic_figures_belong_to_a_capture():
+    """Every figure stands under the commit that its capture ran on; where the
+    history is at hand, that commit's sources have the hash beside it."""
+    commit = None
+    for line in open(os.path.join(bench.ROOT, "profiles", "traffic.txt")):
+        if line.startswith("#"):
+            named = re.search(r"(?:commit |\()([0-9a-f]{7})\b", line)
+            commit = named.group(1) if named else (commit if "commit" not in line and "sources" not in line else None)
+            continue
+        kernel_class, _, digest, nbytes = line.split()
+        assert commit is not None and int(nbytes) > 0, line
+        names = ["jepa_video_encoder_b200/csrc/" + n for n in bench._CLASS_SOURCES.get(kernel_class, bench._GEMM_SOURCES)]
+        got = [subprocess.run(["git", "show", f"{commit}:{n}"], cwd=bench.ROOT, capture_output=True, text=True)
+               for n in names + ["include/jepa_b200.h"]]
+        if all(r.returncode == 0 for r in got):
+            assert bench.hash_sources([r.stdout for r in got]) == digest, line
 
 
 def test_small_configs_are_whole_patches():
