@@ -97,12 +97,14 @@ def test_source_hash_ignores_comments_not_code():
 def test_traffic_figures_belong_to_a_capture():
     """Every figure stands under the commit that its capture ran on; where the
     history is at hand, that commit's sources have the hash beside it."""
-    commit = None
+    commit, figure = None, False
     for line in open(os.path.join(bench.ROOT, "profiles", "traffic.txt")):
         if line.startswith("#"):
             named = re.search(r"(?:commit |\()([0-9a-f]{7})\b", line)
-            commit = named.group(1) if named else (commit if "commit" not in line and "sources" not in line else None)
+            commit = named.group(1) if named else (None if figure else commit)   # a note behind figures opens a new group
+            figure = False
             continue
+        figure = True
         kernel_class, _, digest, nbytes = line.split()
         assert commit is not None and int(nbytes) > 0, line
         names = ["jepa_video_encoder_b200/csrc/" + n for n in bench._CLASS_SOURCES.get(kernel_class, bench._GEMM_SOURCES)]
