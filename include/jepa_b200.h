@@ -532,7 +532,7 @@ JEPA_B200_API int jepa_b200_op_qk_norm_rope(const jepa_b200_qk_norm_rope_args *a
 typedef struct {
   jepa_b200_heads q, k, v, out;
   int dtype, B, Nq, Nk, heads_q, heads_kv, head_dim;
-  float scale, cap;           /* cap 0: none */
+  float scale, cap;           /* finite; cap 0: none, not negative */
   int causal, n_docs;
   const float *slopes;        /* device [heads_q], or NULL */
   const int32_t *prefix;      /* device [B], with documents [B, n_docs]; NULL: none.  Needs causal. */

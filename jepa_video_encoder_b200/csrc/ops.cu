@@ -2,6 +2,7 @@
 // the host and enqueues exactly the kernel the forward pass uses.
 #include <string.h>
 
+#include <cmath>
 #include <mutex>
 
 #include "head_ops.h"
@@ -386,7 +387,7 @@ int jepa_b200_op_masked_attention(const jepa_b200_masked_attention_args* a, void
       a->head_dim < 8 || a->head_dim > 128 || a->head_dim % 8 != 0 || a->B > 65535 || a->heads_q > 65535 ||
       static_cast<long long>(a->B) * a->heads_q > 0x7fffffffll || a->Nq > 0x3fffffff || a->Nk > 0x3fffffff)
     return JEPA_B200_ERR_SHAPE;
-  if (!(a->scale == a->scale) || !(a->cap >= 0.0f) || (a->causal != 0 && a->causal != 1)) return JEPA_B200_ERR_ARG;
+  if (!std::isfinite(a->scale) || !std::isfinite(a->cap) || a->cap < 0.0f || (a->causal != 0 && a->causal != 1)) return JEPA_B200_ERR_ARG;
   if (a->n_docs < 0 || (a->n_docs > 0) != (a->doc_offsets != nullptr) || (a->prefix && !a->causal))
     return JEPA_B200_ERR_ARG;
   if (a->n_docs > 0 && (a->Nq != a->Nk || a->kv_len || a->q_start)) return JEPA_B200_ERR_ARG;

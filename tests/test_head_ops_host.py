@@ -325,6 +325,13 @@ def test_masked_attention_entry_refuses(lib, kw, status):
     assert lib.jepa_b200_op_masked_attention(ctypes.byref(_attn(**kw)), None) == status
 
 
+@pytest.mark.parametrize("kw", [dict(scale=math.inf), dict(scale=-math.inf), dict(cap=math.inf)])
+def test_masked_attention_entry_refuses_infinities(lib, kw):
+    """As the binding does: an infinite scale or cap times a score of zero has
+    no value."""
+    assert lib.jepa_b200_op_masked_attention(ctypes.byref(_attn(B=0, **kw)), None) == _abi.ERR_ARG
+
+
 def test_masked_attention_entry_empty(lib):
     assert lib.jepa_b200_op_masked_attention(None, None) == _abi.ERR_ARG
     assert lib.jepa_b200_op_masked_attention(ctypes.byref(_attn(B=0)), None) == 0
