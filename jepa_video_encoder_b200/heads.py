@@ -57,7 +57,8 @@ def _check_cuda(t, name: str, device: int) -> None:
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
         raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{device}")
-    check_forward_only(t, name)
+    if t.requires_grad or fwAD._current_level >= 0:
+        check_forward_only(t, name)
 
 
 def check_heads(t, name: str, dtype=None, shape: Optional[Sequence[int]] = None, granule: int = 1):
@@ -157,7 +158,7 @@ def _launch(t, stream):
 def _hold(device: int, raw: int, stream, tensors) -> None:
     """Tell the allocator that a stream other than the current one, whose
     memory they are, uses these tensors."""
-    if stream is not None and raw != _raw_stream(device):
+    if raw != _raw_stream(device):
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
@@ -354,7 +355,8 @@ def rope(x, positions, plan: RopePlan, out=None, stream=None):
         check_output(out, "out", [(x, "x", True), (positions, "positions", False)])
     if not (B and N and H):
         return out
-    _hold(device, raw, stream, (x, positions, out))
+    if stream is not None:
+        _hold(device, raw, stream, (x, positions, out))
     check(load_library().jepa_b200_op_rope(_ROPE.pack(*at_x, *at_out, dtype, B, N, H, d, *words), raw), "rope")
     return out
 
@@ -432,7 +434,8 @@ def qk_norm_rope(q, k, positions, plan: Optional[RopePlan], q_weight, k_weight, 
         check_output(k_out, "k_out", [(k, "k", True), (q, "q", False), (q_out, "q_out", False)] + others())
     if not (B and N and (hq or hk)):
         return q_out, k_out
-    _hold(device, raw, stream, (q, k, positions, q_weight, k_weight, q_bias, k_bias, q_out, k_out))
+    if stream is not None:
+        _hold(device, raw, stream, (q, k, positions, q_weight, k_weight, q_bias, k_bias, q_out, k_out))
     check(load_library().jepa_b200_op_qk_norm_rope(
         _QK.pack(*at_q, *at_k, *at_qo, *at_ko, dtype, B, N, hq, hk, d, _NORMS[norm], eps, qw, qb, kw, kb, qw_h, qb_h,
                  kw_h, kb_h, *words), raw), "qk_norm_rope")
@@ -526,7 +529,8 @@ def masked_attention(q, k, v, *, scale: Optional[float] = None, cap: Optional[fl
                                   (q_start, "q_start", False), (slopes, "slopes", False)])
     if not (B and Nq):
         return out
-    _hold(device, raw, stream, (q, k, v, slopes, prefix, doc_offsets, kv_len, q_start, out))
+    if stream is not None:
+        _hold(device, raw, stream, (q, k, v, slopes, prefix, doc_offsets, kv_len, q_start, out))
     check(load_library().jepa_b200_op_masked_attention(
         _ATTN.pack(*at_q, *at_k, *at_v, *at_out, dtype, B, Nq, Nk, hq, hk, d, scale, cap,
                    1 if causal else 0, n_docs, at_slopes, at_prefix, at_docs, at_len, at_start), raw),
