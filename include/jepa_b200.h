@@ -425,11 +425,12 @@ JEPA_B200_API int jepa_b200_op_mean_pool_noalloc(const float *y, int B, int ntok
 /* ------------------------------------------------------------------------
  * Per-head calls: rotary positions, norms of queries and keys, attention
  * under masks.  They stand between a QKV projection and an output projection
- * (jepa_b200_op_linear) and take their operands where these leave them: a
- * tensor [B, N, heads, head_dim] is described by its strides, so that q, k
- * and v may be views of one projection output [B, N, (hq + 2 hk) * head_dim]
- * or of a cache.  They allocate nothing, keep nothing between calls and need
- * no workspace: calls on several streams, and captured graphs of them, are
+ * (jepa_b200_op_linear, which writes F16 or F32; BF16 operands come from
+ * elsewhere) and take their operands where these leave them: a tensor [B, N,
+ * heads, head_dim] is described by its strides, so that q, k and v may be
+ * views of one projection output [B, N, (hq + 2 hk) * head_dim] or of a
+ * cache.  They allocate nothing, keep nothing between calls and need no
+ * workspace: calls on several streams, and captured graphs of them, are
  * independent of one another.  Forward only.
  * ---------------------------------------------------------------------- */
 

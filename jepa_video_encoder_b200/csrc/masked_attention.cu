@@ -171,7 +171,8 @@ __global__ void __launch_bounds__(128) masked_rows_kernel(const MaskedAttnParams
 //
 // What bounds it: heads of 128, the tensor cores (9472 keys, 8 heads, bf16:
 // 287 us, 1280 TFLOP/s, beside 1378 for a matrix product sustained under the
-// power limit); heads of 64, the softmax (247 us, 745 TFLOP/s): a pair of
+// power limit); heads of 64, the softmax (252 us in f16, 729 TFLOP/s; 259 in
+// bf16, whose part of the exponentials costs a product more): a pair of
 // key tiles takes 2900 clocks, in which the special-function unit is busy for
 // half, the issue slots for half and the tensor cores for a third, and the
 // rest is the two softmax warps of a scheduler waiting on the same things.
